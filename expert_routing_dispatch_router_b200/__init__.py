@@ -1,5 +1,6 @@
-"""B200 (sm_100a) library for the forward pass of a mixture-of-experts FFN
-layer with zero-computation (identity) experts: Python binding.
+"""B200 (sm_100a) library for the forward and backward pass of a
+mixture-of-experts FFN layer with zero-computation (identity) experts: Python
+binding.
 
 Every step of the layer runs in the CUDA library ``_lib/libmoe.so`` behind the
 C ABI declared in ``include/moe_api.h``. This module only marshals torch CUDA
@@ -53,6 +54,41 @@ class MoEPIDParams(ctypes.Structure):
                 ("max_step", ctypes.c_float)]
 
 
+class MoEGrouped(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int32), ("groups", ctypes.c_int32),
+                ("n_in", ctypes.c_int32), ("n_out", ctypes.c_int32),
+                ("dtype", ctypes.c_int32)]
+
+
+class MoEAdamW(ctypes.Structure):
+    _fields_ = [("n_tensors", ctypes.c_int32), ("state_bits", ctypes.c_int32),
+                ("param_dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32),
+                ("total_blocks", ctypes.c_int64)]
+
+
+class MoEAdamWParams(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_double) for n in ("lr", "beta1", "beta2", "eps",
+                                               "weight_decay")]
+
+
+_DTYPE_CODE = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
+
+
+@dataclass(frozen=True)
+class GroupedShape:
+    """Sizes of a grouped matrix product (mirrors moe_grouped_t): the capacity
+    of the row buffers, the number of matrices, and their [n_out, n_in]."""
+    rows: int
+    groups: int
+    n_in: int
+    n_out: int
+    dtype: torch.dtype = torch.bfloat16
+
+    def c(self) -> MoEGrouped:
+        return MoEGrouped(self.rows, self.groups, self.n_in, self.n_out,
+                          _DTYPE_CODE[self.dtype])
+
+
 @dataclass(frozen=True)
 class LayerShape:
     """Sizes of one layer call (mirrors moe_config_t)."""
@@ -96,6 +132,7 @@ def lib():
                 "`python -m expert_routing_dispatch_router_b200.build`")
         L = ctypes.CDLL(LIB_PATH)
         C = ctypes.POINTER(MoEConfig)
+        G = ctypes.POINTER(MoEGrouped)
         i32 = ctypes.c_int
         sz = ctypes.c_size_t
         sig = {
@@ -115,6 +152,17 @@ def lib():
             "moe_ep_plan": ([C, ctypes.c_int32, ctypes.c_int32, P, P, P, P], i32),
             "moe_ep_dispatch": ([C, ctypes.c_int32, P, P, P, P, P, P], i32),
             "moe_ep_return": ([C, ctypes.c_int32, ctypes.c_int32, P, P, P, P, P, P], i32),
+            "moe_grouped_workspace_size": ([G], sz),
+            "moe_grouped_matmul": ([G, P, P, P, P, P, sz, P], i32),
+            "moe_grouped_matmul_dx": ([G, P, P, P, P, P, sz, P], i32),
+            "moe_grouped_matmul_dw": ([G, P, P, P, P, i32, P, sz, P], i32),
+            "moe_backward_workspace_size": ([C], sz),
+            "moe_combine_backward": ([C] + [P] * 9, i32),
+            "moe_expert_ffn_backward": ([C] + [P] * 10 + [i32, P, sz, P], i32),
+            "moe_input_backward": ([C] + [P] * 11 + [sz, P], i32),
+            "moe_layer_backward": ([C] + [P] * 17 + [i32, P, sz, P], i32),
+            "moe_adamw_step": ([ctypes.POINTER(MoEAdamW), ctypes.POINTER(MoEAdamWParams)]
+                               + [P] * 7, i32),
             "moe_status_string": ([i32], ctypes.c_char_p),
         }
         for name, (args, res) in sig.items():
@@ -429,3 +477,300 @@ def bias_pid_update(shape: LayerShape, counts, bias, state, target: float, kp: f
                                    _ptr(state), ctypes.byref(prm), _stream(stream))
     _check("moe_bias_pid_update", st)
     return bias, state
+
+
+# ------------------------------------------------------------------ training --
+def alloc_grouped_workspace(shape: GroupedShape, device="cuda") -> torch.Tensor:
+    """Zeroed workspace of the grouped products (one error word)."""
+    n = int(lib().moe_grouped_workspace_size(ctypes.byref(shape.c())))
+    if n == 0:
+        raise ValueError(f"invalid or unsupported shape {shape}")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def _out(t, name, dtype, shape, device):
+    """An output the caller gave (checked), or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _need(t, name, dtype, shape)
+    return t
+
+
+def grouped_matmul(shape: GroupedShape, x, w, offsets, ws, out=None, stream=None):
+    """Ragged products y[r] = w[e] x[r] for the rows r of each segment
+    [offsets[e], offsets[e+1]) -> y [rows, n_out] (rows from offsets[groups] on
+    untouched)."""
+    R, G, I, O = shape.rows, shape.groups, shape.n_in, shape.n_out
+    _need(x, "x", shape.dtype, (R, I))
+    _need(w, "w", shape.dtype, (G, O, I))
+    _need(offsets, "offsets", torch.int32, (G + 1,))
+    out = _out(out, "out", shape.dtype, (R, O), x.device)
+    st = lib().moe_grouped_matmul(ctypes.byref(shape.c()), _ptr(x), _ptr(w), _ptr(offsets),
+                                  _ptr(out), *_ws(ws), _stream(stream))
+    _check("moe_grouped_matmul", st)
+    return out
+
+
+def grouped_matmul_dx(shape: GroupedShape, dy, w, offsets, ws, out=None, stream=None):
+    """Ragged products dx[r] = w[e]^T dy[r] -> dx [rows, n_in]: the input
+    gradient of grouped_matmul (rows from offsets[groups] on untouched)."""
+    R, G, I, O = shape.rows, shape.groups, shape.n_in, shape.n_out
+    _need(dy, "dy", shape.dtype, (R, O))
+    _need(w, "w", shape.dtype, (G, O, I))
+    _need(offsets, "offsets", torch.int32, (G + 1,))
+    out = _out(out, "out", shape.dtype, (R, I), dy.device)
+    st = lib().moe_grouped_matmul_dx(ctypes.byref(shape.c()), _ptr(dy), _ptr(w),
+                                     _ptr(offsets), _ptr(out), *_ws(ws), _stream(stream))
+    _check("moe_grouped_matmul_dx", st)
+    return out
+
+
+def grouped_matmul_dw(shape: GroupedShape, dy, x, offsets, ws, out=None, stream=None):
+    """Ragged products dw[e] = sum over e's rows of dy[r] x[r]^T -> dw [groups,
+    n_out, n_in]: the weight gradient of grouped_matmul, in the operands' type
+    or, when `out` is float32, in fp32. A segment without rows gives zeros."""
+    R, G, I, O = shape.rows, shape.groups, shape.n_in, shape.n_out
+    _need(dy, "dy", shape.dtype, (R, O))
+    _need(x, "x", shape.dtype, (R, I))
+    _need(offsets, "offsets", torch.int32, (G + 1,))
+    f32 = out is not None and out.dtype == torch.float32
+    out = _out(out, "out", torch.float32 if f32 else shape.dtype, (G, O, I), x.device)
+    st = lib().moe_grouped_matmul_dw(ctypes.byref(shape.c()), _ptr(dy), _ptr(x),
+                                     _ptr(offsets), _ptr(out), _DTYPE_CODE[out.dtype],
+                                     *_ws(ws), _stream(stream))
+    _check("moe_grouped_matmul_dw", st)
+    return out
+
+
+def alloc_backward_workspace(shape: LayerShape, device="cuda") -> torch.Tensor:
+    """Workspace of the backward calls (its first 256 bytes zeroed: the error
+    word must start at zero)."""
+    n = int(lib().moe_backward_workspace_size(ctypes.byref(shape.c())))
+    if n == 0:
+        raise ValueError(f"invalid or unsupported shape {shape}")
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    ws[:256].zero_()
+    return ws
+
+
+def combine_backward(shape: LayerShape, dout, x, y_perm, topk_idx, topk_gate, slot_row,
+                     dy_perm=None, dgate=None, stream=None):
+    """Gradients of combine -> (dy_perm [T*k, d], dgate [T, k] f32); rows of
+    dy_perm behind the routed ones are untouched."""
+    T, k, d = shape.T, shape.top_k, shape.d
+    _need(dout, "dout", shape.act_dtype, (T, d))
+    _need(x, "x", shape.act_dtype, (T, d))
+    _need(y_perm, "y_perm", shape.act_dtype, (T * k, d))
+    _need(topk_idx, "topk_idx", torch.int32, (T, k))
+    _need(topk_gate, "topk_gate", torch.float32, (T, k))
+    _need(slot_row, "slot_row", torch.int32, (T * k,))
+    dy_perm = _out(dy_perm, "dy_perm", shape.act_dtype, (T * k, d), x.device)
+    dgate = _out(dgate, "dgate", torch.float32, (T, k), x.device)
+    st = lib().moe_combine_backward(ctypes.byref(shape.c()), _ptr(dout), _ptr(x),
+                                    _ptr(y_perm), _ptr(topk_idx), _ptr(topk_gate),
+                                    _ptr(slot_row), _ptr(dy_perm), _ptr(dgate),
+                                    _stream(stream))
+    _check("moe_combine_backward", st)
+    return dy_perm, dgate
+
+
+def _weight_grads(shape, dw_gate, dw_up, dw_down, device):
+    """The experts' weight gradients (given or new) and their common type: the
+    activation type unless the given ones are float32."""
+    N, F, d = shape.n_routed, shape.ffn, shape.d
+    given = [t for t in (dw_gate, dw_up, dw_down) if t is not None]
+    dtype = given[0].dtype if given else shape.act_dtype
+    if dtype not in (shape.act_dtype, torch.float32):
+        raise ValueError(f"weight gradients: dtype {dtype}, expected {shape.act_dtype} "
+                         "or torch.float32")
+    out = tuple(_out(t, n, dtype, s, device) for n, t, s in (
+        ("dw_gate", dw_gate, (N, F, d)), ("dw_up", dw_up, (N, F, d)),
+        ("dw_down", dw_down, (N, d, F))))
+    return out, _DTYPE_CODE[dtype]
+
+
+def _need_experts(shape, w_gate, w_up, w_down):
+    N, F, d = shape.n_routed, shape.ffn, shape.d
+    for name, w, shp in (("w_gate", w_gate, (N, F, d)), ("w_up", w_up, (N, F, d)),
+                         ("w_down", w_down, (N, d, F))):
+        _need(w, name, shape.act_dtype, shp)
+
+
+def expert_ffn_backward(shape: LayerShape, x_perm, offsets, w_gate, w_up, w_down, dy_perm, ws,
+                        dx_perm=None, dw_gate=None, dw_up=None, dw_down=None, stream=None):
+    """Gradients of expert_ffn -> (dx_perm [T*k, d], dw_gate, dw_up [N, F, d],
+    dw_down [N, d, F]); the pre-activations are computed again. Weight gradients
+    come in the activation type, or in float32 when given as such. Rows of
+    dx_perm behind the routed ones are untouched."""
+    T, k, d = shape.T, shape.top_k, shape.d
+    _need(x_perm, "x_perm", shape.act_dtype, (T * k, d))
+    _need(offsets, "offsets", torch.int32, (shape.n_routed + 1,))
+    _need_experts(shape, w_gate, w_up, w_down)
+    _need(dy_perm, "dy_perm", shape.act_dtype, (T * k, d))
+    dx_perm = _out(dx_perm, "dx_perm", shape.act_dtype, (T * k, d), x_perm.device)
+    dws, code = _weight_grads(shape, dw_gate, dw_up, dw_down, x_perm.device)
+    st = lib().moe_expert_ffn_backward(ctypes.byref(shape.c()), _ptr(x_perm), _ptr(offsets),
+                                       _ptr(w_gate), _ptr(w_up), _ptr(w_down), _ptr(dy_perm),
+                                       _ptr(dx_perm), *[_ptr(t) for t in dws], code,
+                                       *_ws(ws), _stream(stream))
+    _check("moe_expert_ffn_backward", st)
+    return (dx_perm, *dws)
+
+
+def input_backward(shape: LayerShape, dout, x, w_router, topk_idx, topk_gate, slot_row, dgate,
+                   dx_perm, ws, dx=None, dw_router=None, stream=None):
+    """Gradients of the layer input (through the experts, the zero experts and
+    the router) and of the router weights -> (dx [T, d], dw_router [E, d] f32)."""
+    T, k, d, E = shape.T, shape.top_k, shape.d, shape.E
+    _need(dout, "dout", shape.act_dtype, (T, d))
+    _need(x, "x", shape.act_dtype, (T, d))
+    _need(w_router, "w_router", torch.float32, (E, d))
+    _need(topk_idx, "topk_idx", torch.int32, (T, k))
+    _need(topk_gate, "topk_gate", torch.float32, (T, k))
+    _need(slot_row, "slot_row", torch.int32, (T * k,))
+    _need(dgate, "dgate", torch.float32, (T, k))
+    _need(dx_perm, "dx_perm", shape.act_dtype, (T * k, d))
+    dx = _out(dx, "dx", shape.act_dtype, (T, d), x.device)
+    dw_router = _out(dw_router, "dw_router", torch.float32, (E, d), x.device)
+    st = lib().moe_input_backward(ctypes.byref(shape.c()), _ptr(dout), _ptr(x),
+                                  _ptr(w_router), _ptr(topk_idx), _ptr(topk_gate),
+                                  _ptr(slot_row), _ptr(dgate), _ptr(dx_perm), _ptr(dx),
+                                  _ptr(dw_router), *_ws(ws), _stream(stream))
+    _check("moe_input_backward", st)
+    return dx, dw_router
+
+
+def layer_backward(shape: LayerShape, dout, x, w_router, w_gate, w_up, w_down, topk_idx,
+                   topk_gate, offsets, slot_row, x_perm, y_perm, ws, dx=None, dw_router=None,
+                   dw_gate=None, dw_up=None, dw_down=None, stream=None):
+    """The whole layer's backward pass, from what route, dispatch and expert_ffn
+    gave in the forward pass -> (dx, dw_router, dw_gate, dw_up, dw_down).
+    combine_backward, expert_ffn_backward and input_backward in one call, bit
+    for bit."""
+    T, k, d, E, N = shape.T, shape.top_k, shape.d, shape.E, shape.n_routed
+    _need(dout, "dout", shape.act_dtype, (T, d))
+    _need(x, "x", shape.act_dtype, (T, d))
+    _need(w_router, "w_router", torch.float32, (E, d))
+    _need(topk_idx, "topk_idx", torch.int32, (T, k))
+    _need(topk_gate, "topk_gate", torch.float32, (T, k))
+    _need(slot_row, "slot_row", torch.int32, (T * k,))
+    if N > 0:
+        _need_experts(shape, w_gate, w_up, w_down)
+        _need(offsets, "offsets", torch.int32, (N + 1,))
+        _need(x_perm, "x_perm", shape.act_dtype, (T * k, d))
+        _need(y_perm, "y_perm", shape.act_dtype, (T * k, d))
+    dx = _out(dx, "dx", shape.act_dtype, (T, d), x.device)
+    dw_router = _out(dw_router, "dw_router", torch.float32, (E, d), x.device)
+    dws, code = _weight_grads(shape, dw_gate, dw_up, dw_down, x.device)
+    st = lib().moe_layer_backward(ctypes.byref(shape.c()), _ptr(dout), _ptr(x),
+                                  _ptr(w_router), _ptr(w_gate), _ptr(w_up), _ptr(w_down),
+                                  _ptr(topk_idx), _ptr(topk_gate), _ptr(offsets),
+                                  _ptr(slot_row), _ptr(x_perm), _ptr(y_perm), _ptr(dx),
+                                  _ptr(dw_router), *[_ptr(t) for t in dws], code, *_ws(ws),
+                                  _stream(stream))
+    _check("moe_layer_backward", st)
+    return (dx, dw_router, *dws)
+
+
+ADAMW_BLOCK = 256  # elements per state block
+
+
+class AdamW:
+    """The states of an AdamW optimizer over fixed weights and gradient buffers
+    (step it with adamw_step). The tensors are kept alive and updated in place;
+    a step reads whatever the gradient buffers hold then.
+
+    params: float32 or bfloat16 CUDA tensors, one type for all; grads: tensors
+    of the same sizes, one type for all. master: float32 copies of bfloat16
+    weights that the steps update instead (the weights get them rounded).
+    state_bits 32 keeps both moments in float32 (``m``, ``v``); 8 keeps e4m3
+    codes and one scale per 256 elements (``m`` and ``v`` are then (codes,
+    scales); v holds the root of the second moment). The buffers are flat, each
+    tensor padded to whole blocks of 256.
+    """
+
+    def __init__(self, params, grads, state_bits: int = 32, master=None):
+        params, grads = list(params), list(grads)
+        master = list(master) if master is not None else [None] * len(params)
+        if state_bits not in (8, 32):
+            raise ValueError(f"state_bits: {state_bits}, expected 8 or 32")
+        if not params or len(grads) != len(params) or len(master) != len(params):
+            raise ValueError("one gradient (and master) per weight, and at least one weight")
+        pdt, gdt = params[0].dtype, grads[0].dtype
+        for what, dt in (("params", pdt), ("grads", gdt)):
+            if dt not in _DTYPE_CODE:
+                raise ValueError(f"{what}: dtype {dt}, expected float32 or bfloat16")
+        for i, (p, g, w) in enumerate(zip(params, grads, master)):
+            _need(p, f"params[{i}]", pdt)
+            _need(g, f"grads[{i}]", gdt, p.shape)
+            if w is not None:
+                if pdt != torch.bfloat16:
+                    raise ValueError("master: only for bfloat16 weights")
+                _need(w, f"master[{i}]", torch.float32, p.shape)
+            for t in (p, g) if w is None else (p, g, w):
+                if t.device != params[0].device:
+                    raise ValueError("all tensors must be on one device")
+                if t.data_ptr() % 16:
+                    raise ValueError("every tensor must be 16-byte aligned")
+        self._refuse_overlaps([t for t in params + master if t is not None], grads)
+        self.params, self.grads, self.master = params, grads, master
+        self.state_bits = state_bits
+        dev = params[0].device
+        rows, at = [], 0
+        for p, g, w in zip(params, grads, master):
+            rows.append([p.data_ptr(), 0 if w is None else w.data_ptr(), g.data_ptr(),
+                         p.numel(), at, 0])
+            at += -(-p.numel() // ADAMW_BLOCK)
+        # a tensor without elements has no block: it is left out of the table
+        rows = [r for r in rows if r[3] > 0]
+        self.total_blocks = at
+        self._c = MoEAdamW(len(rows), state_bits, _DTYPE_CODE[pdt], _DTYPE_CODE[gdt], at)
+        self._table = torch.tensor(rows, dtype=torch.int64).reshape(-1, 6).to(dev)
+        n = at * ADAMW_BLOCK
+        if state_bits == 32:
+            self.m = torch.zeros(n, device=dev)
+            self.v = torch.zeros(n, device=dev)
+        else:
+            self.m, self.v = ((torch.zeros(n, dtype=torch.float8_e4m3fn, device=dev),
+                               torch.zeros(at, device=dev)) for _ in range(2))
+        self.state = torch.zeros(2, dtype=torch.int64, device=dev)  # step count, scratch
+
+    @staticmethod
+    def _refuse_overlaps(written, read):
+        spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size(), out)
+                       for out, ts in ((1, written), (0, read)) for t in ts if t.numel())
+        end, end_out = 0, 0  # the furthest end so far, of all spans and of written ones
+        for lo, hi, out in spans:
+            if lo < (end if out else end_out):
+                raise ValueError("a weight or master overlaps another tensor")
+            end, end_out = max(end, hi), max(end_out, hi if out else 0)
+
+    def load_state(self, m, v, step: int):
+        """Sets the states (in the layout of ``m`` and ``v``) and the number of
+        steps taken."""
+        for mine, new, name in ((self.m, m, "m"), (self.v, v, "v")):
+            mine, new = (mine, new) if self.state_bits == 8 else ((mine,), (new,))
+            if len(mine) != len(new):
+                raise ValueError(f"{name}: expected (codes, scales)")
+            for a, b in zip(mine, new):
+                _need(b, name, a.dtype, a.shape)
+                a.copy_(b)
+        if step < 0:
+            raise ValueError(f"step: {step}, expected >= 0")
+        self.state[0] = step
+
+
+def adamw_step(opt: AdamW, lr: float, beta1: float = 0.9, beta2: float = 0.999,
+               eps: float = 1e-8, weight_decay: float = 0.0, stream=None):
+    """One AdamW step of every tensor of `opt`, in place, from what its gradient
+    buffers hold. The step count lives on the device, so a step captured in a
+    CUDA graph counts on when it is replayed (its lr and betas are those of the
+    capture)."""
+    hyper = MoEAdamWParams(lr, beta1, beta2, eps, weight_decay)
+    m, ms = opt.m if opt.state_bits == 8 else (opt.m, None)
+    v, vs = opt.v if opt.state_bits == 8 else (opt.v, None)
+    st = lib().moe_adamw_step(ctypes.byref(opt._c), ctypes.byref(hyper), _ptr(opt._table),
+                              _ptr(m), _ptr(ms), _ptr(v), _ptr(vs), _ptr(opt.state),
+                              _stream(stream))
+    _check("moe_adamw_step", st)
+    return opt

@@ -1,0 +1,163 @@
+// Internal declarations of the training operators: grouped products in three
+// directions, the experts' backward pass, and the gradients of the combine and
+// of the layer input.
+#pragma once
+
+#include "moe_internal.cuh"
+
+namespace moe {
+
+// Direction of a grouped product over the row segments of `groups` weight
+// matrices w[e] of [n_out, n_in]:
+//   kFwd  y[r, o]     = sum_i x[r, i] w[e][o, i]
+//   kDx   dx[r, i]    = sum_o dy[r, o] w[e][o, i]
+//   kDw   dw[e][o, i] = sum_{r of e} dy[r, o] x[r, i]
+enum class Form : int { kFwd = 0, kDx = 1, kDw = 2 };
+
+// One product. a holds the rows (x, dy, dy), b the weights (w, w, x). A
+// second pair (kDx only) adds a2 w2 to the same output: the input gradient of
+// two projections that share their input.
+struct GroupedJob {
+  Form form;
+  const void* a;
+  const void* b;
+  const void* a2;
+  const void* b2;
+  void* out;
+  int n_in, n_out;
+  bool out_f32;  // out in float; else in the activation type
+};
+constexpr int kMaxJobs = 3;
+
+struct GroupedShape {
+  int64_t rows;  // capacity of the row buffers
+  int groups;
+  bool bf16;
+};
+
+// Runs independent products over the same segments. err: the workspace error
+// word (bounded waits of the tensor-core kernels).
+cudaError_t launch_grouped_jobs(const GroupedShape& g, const GroupedJob* jobs, int n_jobs,
+                                const int32_t* offsets, int32_t* err, cudaStream_t st);
+// Whether unit numbers of a product fit the kernels' 32-bit counters.
+bool grouped_fits(int64_t rows, int64_t groups, int64_t n_in, int64_t n_out);
+
+// ---- the experts' backward pass and the layer's other gradients ----
+struct BackwardWs {   // byte offsets from the workspace's base
+  size_t header;      // int32[64]: [0] error code
+  size_t pre_a, pre_u;  // float [T*k, F]: pre-activations
+  size_t dh;          // float [T*k, F]: gradient of h
+  size_t h, da, du;   // act [T*k, F]: h and the gradients of the pre-activations
+  size_t dy_perm;     // act [T*k, d]  (whole-layer call)
+  size_t dx_perm;     // act [T*k, d]  (whole-layer call)
+  size_t dgate;       // float [T, k]  (whole-layer call)
+  size_t dlogit;      // float [T, k]
+  size_t dl_row;      // float [T*k]: dlogit in the order of the slot list
+  size_t chunk_base;  // int32 [nchunks, E]
+  size_t counts;      // int32 [E + 1]: slot counts, then the first chunk per expert
+  size_t offsets;     // int32 [E + 1]: slots per expert, zero experts included
+  size_t row_token;   // int32 [T*k]
+  size_t slot_row;    // int32 [T*k]
+  size_t dw_part;     // float [chunks, d] partial router-weight gradients
+  size_t total;
+};
+BackwardWs backward_ws(const Shape& sh);
+
+cudaError_t launch_expert_ffn_backward(const Shape& sh, const void* x_perm,
+                                       const int32_t* offsets, const void* w_gate,
+                                       const void* w_up, const void* w_down,
+                                       const void* dy_perm, void* dx_perm, void* dw_gate,
+                                       void* dw_up, void* dw_down, bool dw_f32, void* ws,
+                                       cudaStream_t st);
+cudaError_t launch_combine_backward(const Shape& sh, const void* dout, const void* x,
+                                    const void* y_perm, const int32_t* idx, const float* gate,
+                                    const int32_t* slot_row, void* dy_perm, float* dgate,
+                                    cudaStream_t st);
+cudaError_t launch_input_backward(const Shape& sh, const void* dout, const void* x,
+                                  const float* w_router, const int32_t* idx, const float* gate,
+                                  const int32_t* slot_row, const float* dgate,
+                                  const void* dx_perm, void* dx, float* dw_router, void* ws,
+                                  cudaStream_t st);
+
+// ---- device helpers ----
+// Segment table of a block in shared memory: s_off[0..n] the row offsets,
+// s_tile[0..n] the prefix sums of ceil(rows / tile). Offsets are clamped to
+// [0, rows] and to be non-decreasing, so no table sends a kernel outside its
+// buffers. All THREADS threads call it; s_warp holds 32 ints. Each thread
+// takes `per` consecutive segments.
+template <int THREADS>
+__device__ __forceinline__ void segment_table(const int32_t* __restrict__ offsets, int n,
+                                              int64_t rows, int tile, int32_t* s_off,
+                                              int32_t* s_tile, int32_t* s_warp) {
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  const int per = (n + THREADS - 1) / THREADS;
+  for (int i = threadIdx.x; i <= n; i += THREADS) {
+    const int32_t o = offsets[i];
+    s_off[i] = o < 0 ? 0 : (o > rows ? (int32_t)rows : o);
+  }
+  __syncthreads();
+  int32_t sum = 0;
+  for (int q = 0; q < per; ++q) {
+    const int e = threadIdx.x * per + q;
+    if (e < n) {
+      const int32_t c = s_off[e + 1] - s_off[e];
+      sum += c > 0 ? (c + tile - 1) / tile : 0;
+    }
+  }
+  int32_t incl = sum;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int32_t o = __shfl_up_sync(0xffffffffu, incl, off);
+    if (lane >= off) incl += o;
+  }
+  if (lane == 31) s_warp[wid] = incl;
+  __syncthreads();
+  int32_t before = incl - sum;
+  for (int w = 0; w < wid; ++w) before += s_warp[w];
+  for (int q = 0; q < per; ++q) {
+    const int e = threadIdx.x * per + q;
+    if (e < n) {
+      s_tile[e] = before;
+      const int32_t c = s_off[e + 1] - s_off[e];
+      before += c > 0 ? (c + tile - 1) / tile : 0;
+      if (e == n - 1) s_tile[n] = before;
+    }
+  }
+  __syncthreads();
+}
+
+// Largest e in [0, n) with s[e] <= v (s non-decreasing, s[0] <= v).
+__device__ __forceinline__ int segment_of(const int32_t* s, int n, int v) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (s[mid] <= v)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  return lo;
+}
+
+// Four consecutive elements (8- or 16-byte aligned) widened to fp32.
+__device__ __forceinline__ float4 load4(const float* p) {
+  return __ldg(reinterpret_cast<const float4*>(p));
+}
+__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
+  const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
+  return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u),
+                     __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
+}
+__device__ __forceinline__ void store4(float* p, float4 v) {
+  *reinterpret_cast<float4*>(p) = v;
+}
+__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
+  const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y);
+  const __nv_bfloat162 b = __floats2bfloat162_rn(v.z, v.w);
+  uint2 o;
+  o.x = *reinterpret_cast<const uint32_t*>(&a);
+  o.y = *reinterpret_cast<const uint32_t*>(&b);
+  *reinterpret_cast<uint2*>(p) = o;
+}
+
+}  // namespace moe

@@ -1,6 +1,7 @@
 /*
- * moe_api.h - C ABI of the B200 (sm_100a) library for the forward pass of a
- * mixture-of-experts FFN layer with zero-computation (identity) experts.
+ * moe_api.h - C ABI of the B200 (sm_100a) library for the forward and backward
+ * pass of a mixture-of-experts FFN layer with zero-computation (identity)
+ * experts.
  *
  * The layer (LongCat-2.0 model card (archdb), section "Mixture of experts";
  * "Meituan lancerer LongCat-2.0" (snilld.dk), section "MoE i praksis og
@@ -276,6 +277,176 @@ typedef struct {
 moe_status_t moe_bias_pid_update(const moe_config_t* cfg, const int32_t* counts,
                                  float* bias, double* state,
                                  const moe_pid_params_t* params, moe_stream_t stream);
+
+/* ------------------------------------------------------------ training --
+ * The layer's backward pass and a weight update. Sizes, layouts, alignment,
+ * streams and errors are those of the forward calls, with these additions:
+ *  - An output may not overlap any other buffer of the call (the workspace
+ *    included): MOE_ERR_INVALID_ARG.
+ *  - No rows: a call without rows writes what a sum over nothing is, zeros in
+ *    its weight gradients, and needs only those pointers (aligned); outputs
+ *    with one row per token or slot are empty.
+ *  - Offsets outside [0, rows] are taken as the nearest bound, and a segment
+ *    that ends before it starts as empty.
+ *  - Sums run in fp32 in an order that does not depend on thread timing. A
+ *    result is rounded once, when it is stored; h and the gradients of the
+ *    pre-activations are also rounded to the activation type, as h is in the
+ *    forward pass.
+ *
+ * Matrix products grouped by expert, in three directions. `groups` matrices
+ * w [groups, n_out, n_in] meet row segments [offsets[e], offsets[e+1]):
+ *   moe_grouped_matmul     y[r]  = w[e] x[r]             y  [rows, n_out]
+ *   moe_grouped_matmul_dx  dx[r] = w[e]^T dy[r]          dx [rows, n_in]
+ *   moe_grouped_matmul_dw  dw[e] = sum_r dy[r] x[r]^T    dw [groups, n_out, n_in]
+ *  x [rows, n_in], dy [rows, n_out], offsets [groups + 1] int32; `rows` is the
+ *  capacity of the row buffers, and rows from offsets[groups] on are neither
+ *  read into a result nor written. A segment without rows gives a zero dw[e].
+ *  dtype is the type of every tensor but the offsets; dw_dtype may also be
+ *  MOE_F32 for bf16 operands (the fp32 sums as they are).
+ *  Limits: 1 <= groups <= 1024, n_in and n_out multiples of 8, and
+ *  (rows / 64 + groups) * (max(n_in, n_out) / 64 + 1) and
+ *  groups * (n_in / 64 + 1) * (n_out / 64 + 1) below 2^31.
+ *  The workspace is one error word: moe_grouped_workspace_size bytes, 256-byte
+ *  aligned, zero before first use, read with moe_read_device_error. */
+typedef struct {
+  int32_t rows;
+  int32_t groups;
+  int32_t n_in;
+  int32_t n_out;
+  moe_dtype_t dtype;
+} moe_grouped_t;
+
+size_t moe_grouped_workspace_size(const moe_grouped_t* shape);
+
+moe_status_t moe_grouped_matmul(const moe_grouped_t* shape, const void* x, const void* w,
+                                const int32_t* offsets, void* y, void* ws, size_t ws_bytes,
+                                moe_stream_t stream);
+
+moe_status_t moe_grouped_matmul_dx(const moe_grouped_t* shape, const void* dy, const void* w,
+                                   const int32_t* offsets, void* dx, void* ws, size_t ws_bytes,
+                                   moe_stream_t stream);
+
+moe_status_t moe_grouped_matmul_dw(const moe_grouped_t* shape, const void* dy, const void* x,
+                                   const int32_t* offsets, void* dw, moe_dtype_t dw_dtype,
+                                   void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/* Bytes of workspace the backward calls of this config need (0 if cfg is
+ * invalid): 256-byte aligned, its first 256 bytes zero before first use. Calls
+ * that share it must be ordered on one stream, as must replays of captured
+ * calls that share it. */
+size_t moe_backward_workspace_size(const moe_config_t* cfg);
+
+/* Gradients of moe_combine with respect to the expert outputs and the gates.
+ *  dout [T, d] act_dtype: gradient of out; x, y_perm, topk_idx, topk_gate and
+ *  slot_row as moe_combine took them.
+ *  dy_perm [T*k, d] act_dtype: s * gate * dout[t] at row slot_row[t, j] of each
+ *          routed slot; rows >= R are left as they were.
+ *  dgate   [T, k] float: s * <dout[t], y_perm[slot_row[t, j]]> for a routed
+ *          slot, <dout[t], x[t]> for a zero-expert slot, 0 for a slot that the
+ *          dispatch skipped (an invalid id, or slot_row < 0 at a routed one).
+ *  x's own gradient through zero-expert slots is part of moe_input_backward. */
+moe_status_t moe_combine_backward(const moe_config_t* cfg, const void* dout, const void* x,
+                                  const void* y_perm, const int32_t* topk_idx,
+                                  const float* topk_gate, const int32_t* slot_row,
+                                  void* dy_perm, float* dgate, moe_stream_t stream);
+
+/* Gradients of moe_expert_ffn. The pre-activations are computed again from
+ * x_perm:
+ *   a = W_gate x, u = W_up x, h = silu(a) u, dh = W_down^T dy,
+ *   da = dh u sig(a) (1 + a (1 - sig(a))),  du = dh silu(a),
+ *   dx = W_gate^T da + W_up^T du,
+ *   dw_gate = sum da x^T, dw_up = sum du x^T, dw_down = sum dy h^T
+ *  x_perm, offsets and the weights as moe_expert_ffn took them; dy_perm
+ *  [T*k, d] act_dtype. dx_perm [T*k, d] act_dtype (rows >= R are left as they
+ *  were); dw_gate, dw_up [N, F, d] and dw_down [N, d, F] in dw_dtype (the
+ *  activation type or MOE_F32), zero for an expert without rows. */
+moe_status_t moe_expert_ffn_backward(const moe_config_t* cfg, const void* x_perm,
+                                     const int32_t* offsets, const void* w_gate,
+                                     const void* w_up, const void* w_down, const void* dy_perm,
+                                     void* dx_perm, void* dw_gate, void* dw_up, void* dw_down,
+                                     moe_dtype_t dw_dtype, void* ws, size_t ws_bytes,
+                                     moe_stream_t stream);
+
+/* Gradients of the layer input and of the router weights, from those of the
+ * gates and of the dispatched rows:
+ *   dl[t, j] = gate (dgate - sum_i gate dgate)          (softmax)
+ *   dx[t]    = sum_{routed j} dx_perm[slot_row[t, j]] + (sum_{zero j} gate) dout[t]
+ *              + sum_j dl[t, j] w_router[idx[t, j]]
+ *   dw_router[e] = sum over the slots of e of dl[t, j] x[t]
+ *  dgate [T, k] float and dx_perm [T*k, d] as the calls above leave them (row
+ *  order of moe_dispatch, also after moe_ep_return); dx [T, d] act_dtype;
+ *  dw_router [E, d] float. The selection and the bias have no gradient. A slot
+ *  with an id outside [0, E) adds nothing to dx and dw_router; the gradients
+ *  of a token that lists an expert twice are unspecified. Both are recorded as
+ *  device error 2. */
+moe_status_t moe_input_backward(const moe_config_t* cfg, const void* dout, const void* x,
+                                const float* w_router, const int32_t* topk_idx,
+                                const float* topk_gate, const int32_t* slot_row,
+                                const float* dgate, const void* dx_perm, void* dx,
+                                float* dw_router, void* ws, size_t ws_bytes,
+                                moe_stream_t stream);
+
+/* The whole layer's backward pass: combine, experts and input backward with
+ * every intermediate in ws, equal to the three calls bit for bit. It takes
+ * what moe_route (topk_idx, topk_gate), moe_dispatch (offsets, slot_row,
+ * x_perm) and moe_expert_ffn (y_perm) gave in the forward pass. Without routed
+ * experts (n_routed = 0) the experts' pointers may be null. */
+moe_status_t moe_layer_backward(const moe_config_t* cfg, const void* dout, const void* x,
+                                const float* w_router, const void* w_gate, const void* w_up,
+                                const void* w_down, const int32_t* topk_idx,
+                                const float* topk_gate, const int32_t* offsets,
+                                const int32_t* slot_row, const void* x_perm, const void* y_perm,
+                                void* dx, float* dw_router, void* dw_gate, void* dw_up,
+                                void* dw_down, moe_dtype_t dw_dtype, void* ws, size_t ws_bytes,
+                                moe_stream_t stream);
+
+/* One AdamW step over many tensors in one launch, run between layer calls.
+ * With t the number of steps after this one:
+ *   m = b1 m + (1 - b1) g          v = b2 v + (1 - b2) g g
+ *   p = (1 - lr wd) p - lr / (1 - b1^t) * m / (sqrt(v) / sqrt(1 - b2^t) + eps)
+ *  table  [n_tensors] moe_adamw_tensor_t, on the device: the weights (and for
+ *         bf16 weights, if wanted, their float masters, which are then what
+ *         the step updates; param gets them rounded), the gradient, the number
+ *         of elements, and the first of the tensor's blocks in the states.
+ *         Blocks hold 256 elements; a tensor of n elements takes ceil(n / 256)
+ *         of them, in ascending order over the table, and no tensor may be
+ *         listed twice. param and grad types are the same for all tensors.
+ *  m, v   the states of total_blocks blocks, zero at the start:
+ *         state_bits 32: float; m_scale and v_scale are not looked at
+ *         state_bits 8:  e4m3 codes of m and of sqrt(v), one byte each, with
+ *         one float per block in m_scale and v_scale (value = code * scale,
+ *         scale = the block's largest magnitude / 448; a positive sqrt(v)
+ *         keeps at least the smallest code)
+ *  state  16 bytes on the device: int64 step count, then scratch. Zero at the
+ *         start; each call adds one, so a captured call counts on when it is
+ *         replayed.
+ *  Returns MOE_ERR_INVALID_ARG for a beta outside [0, 1), a negative or
+ *  non-finite lr or weight_decay, an eps that is not positive, or a bad
+ *  pointer. Host structs are read during the call only. */
+typedef struct {
+  void* param;
+  float* master; /* NULL: param itself is updated */
+  const void* grad;
+  int64_t n;
+  int64_t first_block;
+  int64_t reserved; /* 0 */
+} moe_adamw_tensor_t;
+
+typedef struct {
+  int32_t n_tensors;
+  int32_t state_bits; /* 8 or 32 */
+  moe_dtype_t param_dtype;
+  moe_dtype_t grad_dtype;
+  int64_t total_blocks;
+} moe_adamw_t;
+
+typedef struct {
+  double lr, beta1, beta2, eps, weight_decay;
+} moe_adamw_params_t;
+
+moe_status_t moe_adamw_step(const moe_adamw_t* opt, const moe_adamw_params_t* params,
+                            const moe_adamw_tensor_t* table, void* m, float* m_scale, void* v,
+                            float* v_scale, void* state, moe_stream_t stream);
 
 /* Waits for `stream`, then reads and clears the device-side error word in ws.
  * *code_out (may be NULL) gets 0 when no check failed, else a nonzero code:
