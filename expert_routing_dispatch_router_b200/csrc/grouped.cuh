@@ -35,19 +35,30 @@ struct GroupedShape {
   bool bf16;
 };
 
-// Runs independent products over the same segments. err: the workspace error
-// word (bounded waits of the tensor-core kernels).
+// Runs independent products over the same segments, either all weight gradients
+// or none: bf16 on the tensor cores, float on the CUDA cores. err: the workspace
+// error word (bounded waits of the tensor-core kernels).
 cudaError_t launch_grouped_jobs(const GroupedShape& g, const GroupedJob* jobs, int n_jobs,
                                 const int32_t* offsets, int32_t* err, cudaStream_t st);
+// Its tensor-core parts, and the gate/up product whose epilogue is the SwiGLU
+// backward: from dh (float) it leaves h, da and du.
+cudaError_t launch_grouped_rows_tc(const GroupedShape& g, const GroupedJob& job,
+                                   const int32_t* offsets, int32_t* err, cudaStream_t st);
+cudaError_t launch_grouped_dw_tc(const GroupedShape& g, const GroupedJob* jobs, int n_jobs,
+                                 const int32_t* offsets, int32_t* err, cudaStream_t st);
+cudaError_t launch_swiglu_backward_tc(const GroupedShape& g, const void* x, const void* w_gate,
+                                      const void* w_up, const float* dh, void* h, void* da,
+                                      void* du, int d, int F, const int32_t* offsets,
+                                      int32_t* err, cudaStream_t st);
 // Whether unit numbers of a product fit the kernels' 32-bit counters.
 bool grouped_fits(int64_t rows, int64_t groups, int64_t n_in, int64_t n_out);
 
 // ---- the experts' backward pass and the layer's other gradients ----
 struct BackwardWs {   // byte offsets from the workspace's base
   size_t header;      // int32[64]: [0] error code
-  size_t pre_a, pre_u;  // float [T*k, F]: pre-activations
   size_t dh;          // float [T*k, F]: gradient of h
   size_t h, da, du;   // act [T*k, F]: h and the gradients of the pre-activations
+                      // (float layers: da and du first hold those themselves)
   size_t dy_perm;     // act [T*k, d]  (whole-layer call)
   size_t dx_perm;     // act [T*k, d]  (whole-layer call)
   size_t dgate;       // float [T, k]  (whole-layer call)

@@ -1,5 +1,5 @@
-// Grouped products on the CUDA cores: every form, float and bfloat16 operands,
-// any sizes that are multiples of 8. The float path of the training operators.
+// Grouped products of float operands, on the CUDA cores: every form, any sizes
+// that are multiples of 8.
 //
 // Each output tile of 64 x 64 is one block's work: 16 steps of the contraction
 // at a time go through shared memory (both operands transposed to
@@ -40,8 +40,8 @@ __device__ __forceinline__ void stage(float (*s)[kTile + 4], int line, int kk, f
 }
 
 // acc += A B over one source. lines are tile rows (i) or columns (j).
-template <Form FORM, typename AT>
-__device__ __forceinline__ void accumulate(const AT* __restrict__ a, const AT* __restrict__ b,
+template <Form FORM>
+__device__ __forceinline__ void accumulate(const float* __restrict__ a, const float* __restrict__ b,
                                            int row0, int n_rows, int i0, int j0, int n_in,
                                            int n_out, float (*sa)[kTile + 4],
                                            float (*sb)[kTile + 4], float acc[4][4]) {
@@ -88,7 +88,7 @@ __device__ __forceinline__ void accumulate(const AT* __restrict__ a, const AT* _
   }
 }
 
-template <Form FORM, typename AT>
+template <Form FORM>
 __device__ __forceinline__ void run_tile(const GroupedJob& job, int64_t unit, int groups,
                                          const int32_t* s_off, const int32_t* s_tile,
                                          float (*sa)[kTile + 4], float (*sb)[kTile + 4]) {
@@ -118,12 +118,12 @@ __device__ __forceinline__ void run_tile(const GroupedJob& job, int64_t unit, in
     if (n_rows > kTile) n_rows = kTile;
   }
   const int64_t wn = (int64_t)n_in * n_out;
-  const AT* b = static_cast<const AT*>(job.b) + (FORM == Form::kDw ? 0 : e * wn);
-  accumulate<FORM, AT>(static_cast<const AT*>(job.a), b, row0, n_rows, i0, j0, n_in, n_out, sa,
+  const float* b = static_cast<const float*>(job.b) + (FORM == Form::kDw ? 0 : e * wn);
+  accumulate<FORM>(static_cast<const float*>(job.a), b, row0, n_rows, i0, j0, n_in, n_out, sa,
                        sb, acc);
   if (FORM == Form::kDx && job.a2 != nullptr)
-    accumulate<FORM, AT>(static_cast<const AT*>(job.a2),
-                         static_cast<const AT*>(job.b2) + e * wn, row0, n_rows, i0, j0, n_in,
+    accumulate<FORM>(static_cast<const float*>(job.a2),
+                         static_cast<const float*>(job.b2) + e * wn, row0, n_rows, i0, j0, n_in,
                          n_out, sa, sb, acc);
 #pragma unroll
   for (int p = 0; p < 4; ++p) {
@@ -133,15 +133,11 @@ __device__ __forceinline__ void run_tile(const GroupedJob& job, int64_t unit, in
                              ? e * wn + (int64_t)(i0 + ti + p) * n_in + j0 + tj
                              : (int64_t)(row0 + ti + p) * cols + j0 + tj;
       const float4 v = make_float4(acc[p][0], acc[p][1], acc[p][2], acc[p][3]);
-      if (job.out_f32)
-        store4(static_cast<float*>(job.out) + at, v);
-      else
-        store4(static_cast<AT*>(job.out) + at, v);
+      store4(static_cast<float*>(job.out) + at, v);
     }
   }
 }
 
-template <typename AT>
 __global__ void __launch_bounds__(kSimtThreads)
     grouped_simt_kernel(const __grid_constant__ SimtArgs args) {
   __shared__ __align__(16) float sa[kStep][kTile + 4];
@@ -169,11 +165,11 @@ __global__ void __launch_bounds__(kSimtThreads)
     const GroupedJob& j = args.job[q];
     const int64_t unit = u - first[q];
     if (j.form == Form::kFwd)
-      run_tile<Form::kFwd, AT>(j, unit, args.groups, s_off, s_tile, sa, sb);
+      run_tile<Form::kFwd>(j, unit, args.groups, s_off, s_tile, sa, sb);
     else if (j.form == Form::kDx)
-      run_tile<Form::kDx, AT>(j, unit, args.groups, s_off, s_tile, sa, sb);
+      run_tile<Form::kDx>(j, unit, args.groups, s_off, s_tile, sa, sb);
     else
-      run_tile<Form::kDw, AT>(j, unit, args.groups, s_off, s_tile, sa, sb);
+      run_tile<Form::kDw>(j, unit, args.groups, s_off, s_tile, sa, sb);
   }
 }
 
@@ -198,16 +194,19 @@ cudaError_t launch_grouped_simt(const GroupedShape& g, const GroupedJob* jobs, i
   for (int q = n_jobs; q < kMaxJobs; ++q) a.job[q] = GroupedJob{};
   const int64_t cap = (int64_t)num_sms() * 6;
   const unsigned blocks = (unsigned)(most < 1 ? 1 : (most < cap ? most : cap));
-  return g.bf16 ? launch_pdl(grouped_simt_kernel<__nv_bfloat16>, dim3(blocks),
-                             dim3(kSimtThreads), 0, st, a)
-                : launch_pdl(grouped_simt_kernel<float>, dim3(blocks), dim3(kSimtThreads), 0, st,
-                             a);
+  return launch_pdl(grouped_simt_kernel, dim3(blocks), dim3(kSimtThreads), 0, st, a);
 }
 
 cudaError_t launch_grouped_jobs(const GroupedShape& g, const GroupedJob* jobs, int n_jobs,
                                 const int32_t* offsets, int32_t* err, cudaStream_t st) {
-  (void)err;
-  return launch_grouped_simt(g, jobs, n_jobs, offsets, st);
+  if (!g.bf16) return launch_grouped_simt(g, jobs, n_jobs, offsets, st);
+  if (jobs[0].form == Form::kDw)
+    return launch_grouped_dw_tc(g, jobs, n_jobs, offsets, err, st);
+  for (int q = 0; q < n_jobs; ++q) {
+    const cudaError_t e = launch_grouped_rows_tc(g, jobs[q], offsets, err, st);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 bool grouped_fits(int64_t rows, int64_t groups, int64_t n_in, int64_t n_out) {

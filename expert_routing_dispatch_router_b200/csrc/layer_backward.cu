@@ -163,22 +163,21 @@ cudaError_t combine_backward(const Shape& sh, const void* dout, const void* x, c
 }
 
 // -------------------------------------------------------- SwiGLU backward --
-// From the pre-activations a, u and dh (fp32): h = silu(a) u,
-// da = dh u sig(a) (1 + a (1 - sig(a))), du = dh silu(a), for routed rows.
-// h, da and du are rounded to the activation type, which feeds the products.
-template <typename AT>
+// The float layers' SwiGLU backward, for routed rows: da and du hold the
+// pre-activations a and u and are replaced,
+//   h = silu(a) u, da = dh u sig(a) (1 + a (1 - sig(a))), du = dh silu(a).
 __global__ void __launch_bounds__(256)
-    swiglu_backward_kernel(const float* a, const float* u, const float* dh,
-                           const int32_t* __restrict__ offsets, int N, int64_t rows, int64_t F,
-                           AT* h, AT* da, AT* du) {
+    swiglu_backward_kernel(const float* __restrict__ dh, const int32_t* __restrict__ offsets,
+                           int N, int64_t rows, int64_t F, float* __restrict__ h, float* da,
+                           float* du) {
   griddep_wait();
   griddep_launch_dependents();
   int64_t R = offsets[N];
   if (R > rows) R = rows;
   for (int64_t i = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) * 4; i < R * F;
        i += (int64_t)gridDim.x * blockDim.x * 4) {
-    const float4 av = *reinterpret_cast<const float4*>(a + i);
-    const float4 uv = *reinterpret_cast<const float4*>(u + i);
+    const float4 av = *reinterpret_cast<const float4*>(da + i);
+    const float4 uv = *reinterpret_cast<const float4*>(du + i);
     const float4 gv = *reinterpret_cast<const float4*>(dh + i);
     const float as[4] = {av.x, av.y, av.z, av.w}, us[4] = {uv.x, uv.y, uv.z, uv.w};
     const float gs[4] = {gv.x, gv.y, gv.z, gv.w};
@@ -450,16 +449,14 @@ cudaError_t input_backward(const Shape& sh, const BackwardWs& L, const void* dou
                     (int)sh.E, (int)sh.k, sh.T * sh.k);
 }
 
-template <typename AT>
-cudaError_t swiglu_backward(const Shape& sh, const float* a, const float* u, const float* dh,
-                            const int32_t* offsets, void* h, void* da, void* du,
-                            cudaStream_t st) {
+cudaError_t swiglu_backward(const Shape& sh, const float* dh, const int32_t* offsets, void* h,
+                            void* da, void* du, cudaStream_t st) {
   int64_t blocks = (sh.T * sh.k * sh.F / 4 + 255) / 256;
   const int64_t cap = (int64_t)num_sms() * 8;
   if (blocks > cap) blocks = cap;
-  return launch_pdl(swiglu_backward_kernel<AT>, dim3((unsigned)blocks), dim3(256), 0, st, a, u,
-                    dh, offsets, (int)sh.N, sh.T * sh.k, sh.F, static_cast<AT*>(h),
-                    static_cast<AT*>(da), static_cast<AT*>(du));
+  return launch_pdl(swiglu_backward_kernel, dim3((unsigned)blocks), dim3(256), 0, st, dh,
+                    offsets, (int)sh.N, sh.T * sh.k, sh.F, static_cast<float*>(h),
+                    static_cast<float*>(da), static_cast<float*>(du));
 }
 
 }  // namespace
@@ -475,8 +472,6 @@ BackwardWs backward_ws(const Shape& sh) {
   const size_t Tk = (size_t)(sh.T * sh.k), act = (size_t)sh.es;
   const bool routed = sh.N > 0;
   L.header = take(256);
-  L.pre_a = take(routed ? Tk * sh.F * 4 : 0);
-  L.pre_u = take(routed ? Tk * sh.F * 4 : 0);
   L.dh = take(routed ? Tk * sh.F * 4 : 0);
   L.h = take(routed ? Tk * sh.F * act : 0);
   L.da = take(routed ? Tk * sh.F * act : 0);
@@ -527,19 +522,18 @@ cudaError_t launch_expert_ffn_backward(const Shape& sh, const void* x_perm,
   const BackwardWs L = backward_ws(sh);
   const GroupedShape g{sh.T * sh.k, (int)sh.N, sh.bf16};
   int32_t* err = at<int32_t>(ws, L.header);
-  float* a = at<float>(ws, L.pre_a);
-  float* u = at<float>(ws, L.pre_u);
   float* dh = at<float>(ws, L.dh);
   void *h = at<void>(ws, L.h), *da = at<void>(ws, L.da), *du = at<void>(ws, L.du);
   const int d = (int)sh.d, F = (int)sh.F;
   const GroupedJob pre[3] = {
-      {Form::kFwd, x_perm, w_gate, nullptr, nullptr, a, d, F, true},
-      {Form::kFwd, x_perm, w_up, nullptr, nullptr, u, d, F, true},
-      {Form::kDx, dy_perm, w_down, nullptr, nullptr, dh, F, d, true}};
-  cudaError_t e = launch_grouped_jobs(g, pre, 3, offsets, err, st);
+      {Form::kDx, dy_perm, w_down, nullptr, nullptr, dh, F, d, true},
+      {Form::kFwd, x_perm, w_gate, nullptr, nullptr, da, d, F, true},
+      {Form::kFwd, x_perm, w_up, nullptr, nullptr, du, d, F, true}};
+  cudaError_t e = launch_grouped_jobs(g, pre, sh.bf16 ? 1 : 3, offsets, err, st);
   if (e != cudaSuccess) return e;
-  e = sh.bf16 ? swiglu_backward<__nv_bfloat16>(sh, a, u, dh, offsets, h, da, du, st)
-              : swiglu_backward<float>(sh, a, u, dh, offsets, h, da, du, st);
+  e = sh.bf16 ? launch_swiglu_backward_tc(g, x_perm, w_gate, w_up, dh, h, da, du, d, F, offsets,
+                                          err, st)
+              : swiglu_backward(sh, dh, offsets, h, da, du, st);
   if (e != cudaSuccess) return e;
   const GroupedJob dx{Form::kDx, da, w_gate, du, w_up, dx_perm, d, F, false};
   e = launch_grouped_jobs(g, &dx, 1, offsets, err, st);
