@@ -481,7 +481,7 @@ def bias_pid_update(shape: LayerShape, counts, bias, state, target: float, kp: f
 
 # ------------------------------------------------------------------ training --
 def alloc_grouped_workspace(shape: GroupedShape, device="cuda") -> torch.Tensor:
-    """Zeroed workspace of the grouped products (one error word)."""
+    """Zeroed workspace of the grouped products (the error word and counters)."""
     n = int(lib().moe_grouped_workspace_size(ctypes.byref(shape.c())))
     if n == 0:
         raise ValueError(f"invalid or unsupported shape {shape}")

@@ -29,6 +29,10 @@ struct GroupedJob {
 };
 constexpr int kMaxJobs = 3;
 
+// Workspace header of these calls (int32 words): [0] error code, and the
+// tensor-core kernels' unit counters, which every launch returns to zero.
+constexpr int kUnitCounter = 2;
+
 struct GroupedShape {
   int64_t rows;  // capacity of the row buffers
   int groups;

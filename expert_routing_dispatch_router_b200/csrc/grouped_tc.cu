@@ -65,6 +65,25 @@ __device__ __forceinline__ void tma_load_3d_pair(const CUtensorMap* map, uint32_
       "l"(reinterpret_cast<uint64_t>(map)), "r"(leader_bar), "r"(x), "r"(y), "r"(z), "l"(policy)
       : "memory");
 }
+__device__ __forceinline__ void tma_load_4d(const CUtensorMap* map, uint32_t dst, uint32_t bar,
+                                            int32_t x, int32_t y, int32_t z, int32_t w,
+                                            uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::"
+      "bytes.L2::cache_hint [%0], [%1, {%3, %4, %5, %6}], [%2], %7;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w), "l"(policy)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_4d_pair(const CUtensorMap* map, uint32_t dst,
+                                                 uint32_t leader_bar, int32_t x, int32_t y,
+                                                 int32_t z, int32_t w, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.mbarrier::"
+      "complete_tx::bytes.L2::cache_hint [%0], [%1, {%3, %4, %5, %6}], [%2], %7;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(leader_bar), "r"(x), "r"(y), "r"(z), "r"(w),
+      "l"(policy)
+      : "memory");
+}
 __device__ __forceinline__ void tma_gather4_2d_pair(const CUtensorMap* map, uint32_t dst,
                                                     uint32_t leader_bar, int32_t x, int32_t y0,
                                                     int32_t y1, int32_t y2, int32_t y3,
@@ -122,6 +141,64 @@ __device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t saddr) {
 // Instruction descriptor bits: operand A, operand B is MN-major.
 constexpr uint32_t kAMn = 1u << 15, kBMn = 1u << 16;
 
+// True in one lane of a converged warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p)::"memory");
+  return p != 0;
+}
+
+// Four MMAs over one stage (64 contraction elements): descriptors a and b move
+// on by ASTEP and BSTEP (in 16-byte units) from one to the next. accum is 0 for
+// the first MMA of an accumulator. One statement, so the operands are set up
+// once: an MMA issued by itself took about 90 cycles, whatever its N, and with
+// the commit four of them took as long as the tensor core needs for N = 256.
+template <bool PAIR, int ASTEP, int BSTEP>
+__device__ __forceinline__ void mma_stage(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                          uint32_t accum) {
+  if (PAIR)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t"
+        "setp.eq.b32 p, 0, 0;\n\t"
+        "add.s64 a, %1, %5;\n\tadd.s64 b, %2, %6;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %3, p;\n\t"
+        "add.s64 a, a, %5;\n\tadd.s64 b, b, %6;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %3, p;\n\t"
+        "add.s64 a, a, %5;\n\tadd.s64 b, b, %6;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accum), "n"(ASTEP), "n"(BSTEP)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+        "setp.eq.b32 p, 0, 0;\n\t"
+        "add.s64 a, %1, %5;\n\tadd.s64 b, %2, %6;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t"
+        "add.s64 a, a, %5;\n\tadd.s64 b, b, %6;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t"
+        "add.s64 a, a, %5;\n\tadd.s64 b, b, %6;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accum), "n"(ASTEP), "n"(BSTEP)
+        : "memory");
+}
+
+// Arrive on another CTA's mbarrier where nothing in memory passes to it (an
+// accumulator has been read, a ring slot taken): release at CTA scope. At
+// cluster scope the arrive would first wait for every store this warp has in
+// flight.
+__device__ __forceinline__ void mbar_arrive_remote_light(uint32_t cluster_bar) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar)
+               : "memory");
+}
+
 // The same operations on one CTA or, from the leader, on a CTA pair. Copies of
 // a pair complete on the leader's barrier; commits arrive in both CTAs.
 template <bool PAIR>
@@ -136,9 +213,9 @@ struct Cg<false> {
                                  int32_t y, int32_t z, uint64_t pol) {
     tma_load_3d(m, dst, bar, x, y, z, pol);
   }
-  __device__ static void gather4(const CUtensorMap* m, uint32_t dst, uint32_t bar, int32_t x,
-                                 int32_t y0, int32_t y1, int32_t y2, int32_t y3, uint64_t pol) {
-    ptx::tma_gather4_2d(m, dst, bar, x, y0, y1, y2, y3, pol);
+  __device__ static void load_4d(const CUtensorMap* m, uint32_t dst, uint32_t bar, int32_t x,
+                                 int32_t y, int32_t z, int32_t w, uint64_t pol) {
+    tma_load_4d(m, dst, bar, x, y, z, w, pol);
   }
   __device__ static void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
     ptx::mma_bf16(d, a, b, idesc, acc);
@@ -162,6 +239,10 @@ struct Cg<true> {
   __device__ static void load_3d(const CUtensorMap* m, uint32_t dst, uint32_t bar, int32_t x,
                                  int32_t y, int32_t z, uint64_t pol) {
     tma_load_3d_pair(m, dst, bar, x, y, z, pol);
+  }
+  __device__ static void load_4d(const CUtensorMap* m, uint32_t dst, uint32_t bar, int32_t x,
+                                 int32_t y, int32_t z, int32_t w, uint64_t pol) {
+    tma_load_4d_pair(m, dst, bar, x, y, z, w, pol);
   }
   __device__ static void gather4(const CUtensorMap* m, uint32_t dst, uint32_t bar, int32_t x,
                                  int32_t y0, int32_t y1, int32_t y2, int32_t y3, uint64_t pol) {
@@ -199,6 +280,30 @@ __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity,
   }
 }
 
+// The same by a whole warp; every lane gets the same answer.
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                          int32_t* err) {
+  return __all_sync(0xffffffffu, wait_bounded(bar, parity, abort_flag, err));
+}
+
+// The same with cluster-scope acquire, for a phase that the other CTA of the
+// pair completes after writing here.
+__device__ __forceinline__ bool wait_bounded_cluster(uint32_t bar, uint32_t parity,
+                                                     volatile int* abort_flag, int32_t* err) {
+  if (ptx::mbar_try_wait_cluster(bar, parity)) return true;
+  const uint64_t t0 = ptx::global_timer_ns();
+  while (true) {
+    for (int i = 0; i < 64; ++i)
+      if (ptx::mbar_try_wait_cluster(bar, parity)) return true;
+    if (*abort_flag) return false;
+    if (ptx::global_timer_ns() - t0 > kWaitLimitNs) {
+      *abort_flag = 1;
+      atomicCAS(err, 0, kErrWaitTimeout);
+      return false;
+    }
+  }
+}
+
 // Bounded wait that ignores the stop flag (used while cleaning up).
 __device__ __forceinline__ void wait_cleanup(uint32_t bar, uint32_t parity) {
   const uint64_t t0 = ptx::global_timer_ns();
@@ -211,22 +316,91 @@ __device__ __forceinline__ void settle_ns(uint64_t ns) {
   }
 }
 
-// The barriers and small state behind the ring, common to both kernels.
+constexpr int kRing = 4;  // units handed out ahead
+constexpr uint32_t kCtlBytes = 320;
+
+// The barriers and small state behind the ring of operand tiles, and the hand
+// -out of work units, common to both kernels. Units are taken in order from a
+// counter in the workspace, so CTAs whose units were short take more of them.
+// The (leader's) producer publishes each unit id, -1 at the end, in a ring of
+// kRing slots in its own and its peer's shared memory; the other roles read
+// their units from there. A slot is free again when its readers have arrived on
+// the publisher's ring_empty: the MMA thread, the epilogue warps and, in a
+// pair, the peer's producer and epilogue warps. The last CTA (pair) to finish
+// returns the counters to zero.
 template <int S, bool PAIR>
 struct Control {
   uint32_t bars;
   volatile int* abort_flag;
   uint32_t* tmem_slot;
+  volatile int* ring;
+  __device__ uint32_t ring_full(int r) const { return bars + 224u + 8u * r; }
+  __device__ uint32_t ring_empty(int r) const { return bars + 256u + 8u * r; }
+  // counters: [0] next unit, [1] CTAs (pairs) that have finished
+  __device__ bool publish(int seq, int u, int32_t* err) const {
+    const int r = seq % kRing;
+    const uint32_t par = (uint32_t)(seq / kRing) & 1u;
+    if (!wait_bounded(ring_empty(r), par ^ 1u, abort_flag, err)) return false;
+    ring[r] = u;
+    if (PAIR) {
+      ptx::st_shared_cluster_u32(
+          ptx::map_to_rank(ptx::smem_addr(const_cast<const int*>(ring + r)), 1), (uint32_t)u);
+      ptx::mbar_arrive_remote(ptx::map_to_rank(ring_full(r), 1));
+    }
+    ptx::mbar_arrive(ring_full(r));
+    return true;
+  }
+  __device__ bool take(int seq, int* u, int32_t* err) const {
+    const int r = seq % kRing;
+    const uint32_t par = (uint32_t)(seq / kRing) & 1u;
+    if (PAIR ? !wait_bounded_cluster(ring_full(r), par, abort_flag, err)
+             : !wait_bounded(ring_full(r), par, abort_flag, err))
+      return false;
+    *u = ring[r];
+    if (PAIR && Cg<PAIR>::rank() != 0)
+      mbar_arrive_remote_light(ptx::map_to_rank(ring_empty(r), 0));
+    else
+      ptx::mbar_arrive(ring_empty(r));
+    return true;
+  }
+  // Next unit for the producer warp: the leader publishes the one it claimed
+  // before, then claims another (after the arrivals, which would wait for the
+  // atomic's return); the peer reads it.
+  __device__ bool next(int seq, int total, int32_t* counters, int* claimed, int* u,
+                       int32_t* err) const {
+    if (PAIR && Cg<PAIR>::rank() != 0) return take_warp(seq, u, err);
+    int v = -1;
+    bool ok = true;
+    if ((threadIdx.x & 31) == 0) {
+      v = seq == 0 ? atomicAdd(counters, 1) : *claimed;
+      if (v >= total) v = -1;
+      ok = publish(seq, v, err);
+      if (v >= 0) *claimed = atomicAdd(counters, 1);
+    }
+    ok = __shfl_sync(0xffffffffu, ok, 0);
+    *u = __shfl_sync(0xffffffffu, v, 0);
+    return ok;
+  }
+  // The same for a whole warp: lane 0 reads, all lanes get it.
+  __device__ bool take_warp(int seq, int* u, int32_t* err) const {
+    int v = -1;
+    bool ok = true;
+    if ((threadIdx.x & 31) == 0) ok = take(seq, &v, err);
+    ok = __shfl_sync(0xffffffffu, ok, 0);
+    *u = __shfl_sync(0xffffffffu, v, 0);
+    return ok;
+  }
   __device__ uint32_t full(int s) const { return bars + 8u * s; }
   __device__ uint32_t empty(int s) const { return bars + 8u * (S + s); }
   __device__ uint32_t tfull(int b) const { return bars + 8u * (2 * S + b); }
   __device__ uint32_t tempty(int b) const { return bars + 8u * (2 * S + 2 + b); }
   __device__ uint32_t mma_done() const { return bars + 8u * (2 * S + 4); }
   __device__ void init(uint8_t* smem, uint32_t sbase, uint32_t bar_off) {
-    static_assert(8 * (2 * S + 5) + 8 <= 256, "barriers fit their 256 bytes");
+    static_assert(8 * (2 * S + 5) + 8 <= 224, "barriers fit their bytes");
     bars = sbase + bar_off;
     tmem_slot = reinterpret_cast<uint32_t*>(smem + bar_off + 8 * (2 * S + 5));
     abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    ring = reinterpret_cast<volatile int*>(smem + bar_off + 288);
     if (threadIdx.x == 0) {
       for (int s = 0; s < S; ++s) {
         ptx::mbar_init(full(s), 1);
@@ -237,6 +411,10 @@ struct Control {
         ptx::mbar_init(tempty(b), PAIR ? 2 * kEpiWarps : kEpiWarps);
       }
       ptx::mbar_init(mma_done(), 1);
+      for (int r = 0; r < kRing; ++r) {
+        ptx::mbar_init(ring_full(r), 1);
+        ptx::mbar_init(ring_empty(r), 1 + kEpiWarps + (PAIR ? 1 + kEpiWarps : 0));
+      }
       *abort_flag = 0;
       ptx::fence_mbar_init();
     }
@@ -247,8 +425,8 @@ struct Control {
     ptx::tc_fence_before();
     __syncwarp();
     if (lane == 0) {
-      if (PAIR)
-        ptx::mbar_arrive_remote(ptx::map_to_rank(tempty(b), 0));
+      if (PAIR && Cg<PAIR>::rank() != 0)
+        mbar_arrive_remote_light(ptx::map_to_rank(tempty(b), 0));
       else
         ptx::mbar_arrive(tempty(b));
     }
@@ -263,10 +441,17 @@ struct Control {
       settle_ns(2000000);
     }
   }
-  __device__ void finish(uint32_t tmem_base) const {
+  __device__ void finish(uint32_t tmem_base, int32_t* counters) const {
     ptx::tc_fence_before();
     __syncthreads();
     Cg<PAIR>::sync_all();  // neither CTA frees TMEM or exits while the pair works
+    if (threadIdx.x == 0 && Cg<PAIR>::rank() == 0) {
+      const int teams = (int)gridDim.x / (PAIR ? 2 : 1);
+      if (atomicAdd(counters + 1, 1) == teams - 1) {  // nobody claims units any more
+        counters[0] = 0;
+        counters[1] = 0;
+      }
+    }
     if ((threadIdx.x >> 5) == 1) {
       ptx::tc_fence_after();
       Cg<PAIR>::dealloc(tmem_base);
@@ -275,28 +460,30 @@ struct Control {
 };
 
 // ------------------------------------------------------------ row products --
-enum class Mode : int { kFwd = 0, kDx = 1, kGateUp = 2 };
+enum class Mode : int { kFwd, kDx, kDxF32, kGateUp };
+__host__ __device__ constexpr bool is_dx(Mode m) { return m == Mode::kDx || m == Mode::kDxF32; }
 
 struct RowArgs {
   const int32_t* offsets;
   int32_t* err;
+  int32_t* counters;  // two, zero between launches
   int64_t rows;
   int groups;
   int cols;      // output columns
   int k_blocks;  // per source
+  bool wide_w;   // kDx: both 64-column blocks of a weight tile come in one copy
   int sources;   // 2: a second (weights, rows) pair extends the contraction
-  void* out;     // bf16 or float rows; kGateUp: h
-  bool out_f32;
+  void* out;     // bf16 rows (kDxF32: float; kGateUp: h)
   // kGateUp only
   const float* dh;
   __nv_bfloat16* da;
   __nv_bfloat16* du;
 };
 
+constexpr int kRowBoxes = 4;  // boxes of 128, 64, 32 and 16 rows
 struct RowMaps {
-  CUtensorMap w[2];     // weights (kGateUp: gate, up; kDx: the two sources)
-  CUtensorMap r16[2];   // rows, 16 per box
-  CUtensorMap r128[2];  // rows, 128 per box
+  CUtensorMap w[2];  // weights (kGateUp: gate, up; kDx: the two sources)
+  CUtensorMap r[2][kRowBoxes];
 };
 
 template <Mode MODE, int BN_, bool PAIR_>
@@ -306,13 +493,13 @@ struct RowCfg {
   static constexpr int BN = BN_;
   static constexpr int BNH = BN / kCtas;  // rows one CTA loads
   static constexpr int kNumA = MODE == Mode::kGateUp ? 2 : 1;
-  static_assert(BN <= 256 && BN % (16 * kCtas) == 0 && BNH <= 128 + 128 * (1 - (kCtas - 1)), "");
+  static_assert(BNH <= 128 && BN % (16 * kCtas) == 0, "rows of a unit");
   static constexpr uint32_t kAccCols = kNumA * BN;
   static constexpr int kAccBufs = kAccCols <= kAccStride ? 2 : 1;
   static constexpr uint32_t kStageBytes = kNumA * kTileBytes + BNH * BK * 2;
   static constexpr int kStages = 204800 / kStageBytes > 8 ? 8 : (int)(204800 / kStageBytes);
   static constexpr uint32_t kBarOff = kStages * kStageBytes;
-  static constexpr uint32_t kTabOff = kBarOff + 256;
+  static constexpr uint32_t kTabOff = kBarOff + kCtlBytes;
   static constexpr uint32_t kSmemBytes = 1024 + kTabOff + 2 * 4 * (kMaxExperts + 1) + 128;
 };
 
@@ -371,8 +558,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t rank = G::rank();
   if (warp == 0 && lane == 0) {
     ptx::prefetch_tensormap(&maps.w[0]);
-    ptx::prefetch_tensormap(&maps.r16[0]);
-    ptx::prefetch_tensormap(&maps.r128[0]);
+    ptx::prefetch_tensormap(&maps.r[0][0]);
+    ptx::prefetch_tensormap(&maps.r[0][kRowBoxes - 1]);
   }
   // everything above overlaps the previous kernel's tail
   griddep_wait();
@@ -385,112 +572,118 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(ctl.tmem_slot);
   const int m_tiles = (args.cols + BM * C::kCtas - 1) / (BM * C::kCtas);
   const int total = s_tile[args.groups] * m_tiles;
-  const int first = (int)blockIdx.x / C::kCtas, stride = (int)gridDim.x / C::kCtas;
   const int n_kb = args.k_blocks * args.sources;
 
   if (warp == 0) {
     // ---------------------------------------------------- TMA producer --
-    if (lane == 0) {
-      const uint64_t pol_first = ptx::policy_evict_first();
-      const uint64_t pol_normal = ptx::policy_evict_normal();
-      int stage = 0;
-      uint32_t phase = 0, armed = 0, armed_par = 0;
-      bool ok = true;
-      for (int u = first; u < total && ok; u += stride) {
-        const RowUnit un = row_unit<BN, STEP>(u, s_tile, s_off, args.groups, m_tiles);
-        const int half = un.n_mma / C::kCtas;
-        const int col0 = (un.m * C::kCtas + (int)rank) * BM;
-        const int brow = un.row0 + (int)rank * half;
-        const uint32_t bytes =
-            (uint32_t)C::kCtas * (C::kNumA * kTileBytes + (uint32_t)half * 128u);
-        // weights that only this unit reads (one row tile) are streamed
-        const uint64_t pol_w = un.ntiles == 1 ? pol_first : pol_normal;
-        for (int kb = 0; kb < n_kb; ++kb) {
-          if (!wait_bounded(ctl.empty(stage), phase ^ 1u, ctl.abort_flag, args.err)) {
-            ok = false;
-            break;
-          }
-          const int src = kb >= args.k_blocks ? 1 : 0;
-          const int k0 = (kb - src * args.k_blocks) * BK;
+    // The warp stays converged and one lane issues.
+    const bool elected = elect_one();
+    const uint64_t pol_first = ptx::policy_evict_first();
+    const uint64_t pol_normal = ptx::policy_evict_normal();
+    const uint32_t full0 = G::at_leader(ctl.full(0));
+    int stage = 0, claimed = 0;
+    uint32_t phase = 0, armed = 0, armed_par = 0;
+    bool ok = true;
+    for (int seq = 0, u; ok; ++seq) {
+      ok = ctl.next(seq, total, args.counters, &claimed, &u, args.err);
+      if (!ok || u < 0) break;
+      const RowUnit un = row_unit<BN, STEP>(u, s_tile, s_off, args.groups, m_tiles);
+      const int half = un.n_mma / C::kCtas;
+      const int col0 = (un.m * C::kCtas + (int)rank) * BM;
+      const int brow = un.row0 + (int)rank * half;
+      const uint32_t bytes = (uint32_t)C::kCtas * (C::kNumA * kTileBytes + (uint32_t)half * 128u);
+      // weights that only this unit reads (one row tile) are streamed
+      const uint64_t pol_w = un.ntiles == 1 ? pol_first : pol_normal;
+      for (int kb = 0; kb < n_kb; ++kb) {
+        if (!(ok = wait_warp(ctl.empty(stage), phase ^ 1u, ctl.abort_flag, args.err))) break;
+        const int src = kb >= args.k_blocks ? 1 : 0;
+        const int k0 = (kb - src * args.k_blocks) * BK;
+        if (elected) {
           if (rank == 0) ptx::mbar_arrive_expect_tx(ctl.full(stage), bytes);
-          const uint32_t fb = G::at_leader(ctl.full(stage));
+          const uint32_t fb = full0 + 8u * stage;
           const uint32_t a0 = sbase + stage * C::kStageBytes;
-          if (MODE == Mode::kDx) {
-            G::load_3d(&maps.w[src], a0, fb, col0, k0, un.e, pol_w);
-            G::load_3d(&maps.w[src], a0 + kBlockBytes, fb, col0 + 64, k0, un.e, pol_w);
-          } else {
+          if (!is_dx(MODE)) {
             G::load_3d(&maps.w[0], a0, fb, k0, col0, un.e, pol_w);
             if (MODE == Mode::kGateUp)
               G::load_3d(&maps.w[1], a0 + kTileBytes, fb, k0, col0, un.e, pol_w);
+          } else if (args.wide_w) {
+            G::load_4d(&maps.w[src], a0, fb, 0, k0, col0 / 64, un.e, pol_w);
+          } else {
+            G::load_3d(&maps.w[src], a0, fb, col0, k0, un.e, pol_w);
+            G::load_3d(&maps.w[src], a0 + kBlockBytes, fb, col0 + 64, k0, un.e, pol_w);
           }
-          const uint32_t b0 = a0 + C::kNumA * kTileBytes;
-          int j = 0;
-          for (; j + 128 <= half; j += 128)
-            G::load_2d(&maps.r128[src], b0 + j * 128u, fb, k0, brow + j, pol_normal);
-          for (; j < half; j += 16)
-            G::load_2d(&maps.r16[src], b0 + j * 128u, fb, k0, brow + j, pol_normal);
-          armed |= 1u << stage;
-          armed_par = (armed_par & ~(1u << stage)) | (phase << stage);
-          if (++stage == S) {
-            stage = 0;
-            phase ^= 1u;
+          uint32_t b0 = a0 + C::kNumA * kTileBytes;
+          int j = brow;
+#pragma unroll
+          for (int q = 0; q < kRowBoxes; ++q) {
+            const int h = 128 >> q;
+            if (half & h) {
+              G::load_2d(&maps.r[src][q], b0, fb, k0, j, pol_normal);
+              b0 += h * 128u;
+              j += h;
+            }
           }
         }
+        armed |= 1u << stage;
+        armed_par = (armed_par & ~(1u << stage)) | (phase << stage);
+        if (++stage == S) {
+          stage = 0;
+          phase ^= 1u;
+        }
       }
-      if (!ok) ctl.settle_loads(armed, armed_par);
     }
+    if (!ok && elected) ctl.settle_loads(armed, armed_par);
+    __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------ MMA issuer --
-    if (lane == 0 && rank == 0) {
+    // The warp stays converged and one lane issues.
+    if (rank == 0) {
+      const bool elected = elect_one();
+      const uint64_t hi_k = ptx::desc_k_sw128(0), hi_mn = desc_mn_sw128(0);
+      constexpr uint32_t kAStep = is_dx(MODE) ? 2048 / 16 : 32 / 16;
       int stage = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true, issued = false;
-      for (int u = first; u < total && ok; u += stride) {
+      for (int seq = 0, u; ok; ++seq) {
+        ok = ctl.take_warp(seq, &u, args.err);
+        if (!ok || u < 0) break;
         const RowUnit un = row_unit<BN, STEP>(u, s_tile, s_off, args.groups, m_tiles);
-        if (!wait_bounded(ctl.tempty(acc), acc_phase ^ 1u, ctl.abort_flag, args.err)) {
-          ok = false;
-          break;
-        }
+        if (!(ok = wait_warp(ctl.tempty(acc), acc_phase ^ 1u, ctl.abort_flag, args.err))) break;
         ptx::tc_fence_after();
         const uint32_t idesc = ptx::idesc_bf16_f32(BM * C::kCtas, un.n_mma) |
-                               (MODE == Mode::kDx ? kAMn : 0u);
+                               (is_dx(MODE) ? kAMn : 0u);
         const uint32_t d0 = tmem_base + (uint32_t)acc * kAccStride;
         for (int kb = 0; kb < n_kb; ++kb) {
-          if (!wait_bounded(ctl.full(stage), phase, ctl.abort_flag, args.err)) {
-            ok = false;
-            break;
-          }
+          if (!(ok = wait_warp(ctl.full(stage), phase, ctl.abort_flag, args.err))) break;
           ptx::tc_fence_after();
-          const uint32_t a0 = sbase + stage * C::kStageBytes;
-          const uint32_t b0 = a0 + C::kNumA * kTileBytes;
-#pragma unroll
-          for (int kk = 0; kk < BK / 16; ++kk) {
-            const uint64_t bdesc = ptx::desc_k_sw128(b0 + kk * 32);
-            const uint64_t adesc = MODE == Mode::kDx ? desc_mn_sw128(a0 + kk * 2048)
-                                                     : ptx::desc_k_sw128(a0 + kk * 32);
-            const uint32_t accum = (kb | kk) != 0 ? 1u : 0u;
-            G::mma(d0, adesc, bdesc, idesc, accum);
+          if (elected) {
+            const uint64_t a = (is_dx(MODE) ? hi_mn : hi_k) | ((sbase + stage * C::kStageBytes) >> 4);
+            const uint64_t b =
+                hi_k | ((sbase + stage * C::kStageBytes + C::kNumA * kTileBytes) >> 4);
+            mma_stage<PAIR, kAStep, 2>(d0, a, b, idesc, kb != 0 ? 1u : 0u);
             if (MODE == Mode::kGateUp)
-              G::mma(d0 + BN, ptx::desc_k_sw128(a0 + kTileBytes + kk * 32), bdesc, idesc, accum);
+              mma_stage<PAIR, kAStep, 2>(d0 + BN, a + (kTileBytes >> 4), b, idesc,
+                                         kb != 0 ? 1u : 0u);
+            G::commit(ctl.empty(stage));
           }
           issued = true;
-          G::commit(ctl.empty(stage));
           if (++stage == S) {
             stage = 0;
             phase ^= 1u;
           }
         }
         if (!ok) break;
-        G::commit(ctl.tfull(acc));
+        if (elected) G::commit(ctl.tfull(acc));
         if (++acc == C::kAccBufs) {
           acc = 0;
           acc_phase ^= 1u;
         }
       }
-      if (!ok && issued) {  // MMAs already issued must finish before TMEM is freed
+      if (!ok && issued && elected) {  // MMAs already issued finish before TMEM is freed
         G::commit(ctl.mma_done());
         wait_cleanup(ctl.mma_done(), 0);
       }
+      __syncwarp();
     }
   } else {
     // -------------------------------------------------------- epilogue --
@@ -498,72 +691,140 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int eh = (warp - 2) >> 2;  // which half of the column chunks
     int acc = 0;
     uint32_t acc_phase = 0;
-    for (int u = first; u < total; u += stride) {
+    for (int seq = 0, u; ctl.take_warp(seq, &u, args.err) && u >= 0; ++seq) {
       const RowUnit un = row_unit<BN, STEP>(u, s_tile, s_off, args.groups, m_tiles);
-      const bool ok = wait_bounded(ctl.tfull(acc), acc_phase, ctl.abort_flag, args.err);
-      if (!__all_sync(0xffffffffu, ok)) break;
-      ptx::tc_fence_after();
-      const uint32_t tb =
-          tmem_base + (static_cast<uint32_t>(ew * 32) << 16) + (uint32_t)acc * kAccStride;
       const int col = (un.m * C::kCtas + (int)rank) * BM + ew * 32 + lane;
-      const bool col_ok = col < args.cols;
       const int64_t obase = (int64_t)un.row0 * args.cols + col;
-      // 32-row chunks, alternating between the two warps of this quarter
-      for (int c0 = 32 * eh; c0 < un.n_mma; c0 += 64) {
-        if (MODE == Mode::kGateUp) {
-          float a[32], v[32], g[32];
-#pragma unroll
-          for (int c = 0; c < 32; ++c)
-            g[c] = col_ok && c0 + c < un.n_valid
-                       ? __ldg(args.dh + obase + (int64_t)(c0 + c) * args.cols)
-                       : 0.f;
-          ptx::tmem_ld32x2(tb + c0, tb + BN + c0, a, v);
-          __nv_bfloat16* h = static_cast<__nv_bfloat16*>(args.out) + obase;
-          __nv_bfloat16* da = args.da + obase;
-          __nv_bfloat16* du = args.du + obase;
+      const int n_out = col < args.cols ? un.n_valid : 0;  // rows this lane stores
+      auto full = [&]() -> bool {
+        const bool ok = wait_bounded(ctl.tfull(acc), acc_phase, ctl.abort_flag, args.err);
+        if (!__all_sync(0xffffffffu, ok)) return false;
+        ptx::tc_fence_after();
+        return true;
+      };
+      const uint32_t tb = tmem_base + (static_cast<uint32_t>(ew * 32) << 16) +
+                          (uint32_t)acc * kAccStride + 32u * eh;
+      // 32-row chunks, alternating between the two warps of this quarter: chunk
+      // q covers rows 64 q + 32 eh ..
+      const int r0 = 32 * eh;
+      if (MODE == Mode::kGateUp) {
+        // dh of a chunk is fetched ahead: the first while the unit's products
+        // still run, the others before the previous chunk's stores. The
+        // accumulator goes back as soon as the last chunk has left TMEM.
+        float g[32];
+        auto fetch = [&](int q) {
 #pragma unroll
           for (int c = 0; c < 32; ++c) {
-            if (col_ok && c0 + c < un.n_valid) {
-              const int64_t at = (int64_t)(c0 + c) * args.cols;
-              const float sig = sigmoid_f(a[c]);
-              const float silu = a[c] * sig;
-              h[at] = __float2bfloat16_rn(silu * v[c]);
-              da[at] = __float2bfloat16_rn(g[c] * v[c] * (sig + silu * (1.0f - sig)));
-              du[at] = __float2bfloat16_rn(g[c] * silu);
+            const int r = 64 * q + r0 + c;
+            g[c] = r < n_out ? __ldg(args.dh + obase + (int64_t)r * args.cols) : 0.f;
+          }
+        };
+        fetch(0);
+        if (!full()) break;
+#pragma unroll 1
+        for (int q = 0; 64 * q < un.n_mma; ++q) {
+          const bool last = 64 * (q + 1) >= un.n_mma;
+          const bool live = 64 * q + r0 < un.n_mma;  // warp-uniform
+          uint32_t h2[16], da2[16], du2[16];
+          if (live) {
+            float a[32], v[32];
+            ptx::tmem_ld32x2(tb + 64 * q, tb + BN + 64 * q, a, v);
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+              float x[2], y[2], z[2];
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const int k = 2 * c + i;
+                const float sig = sigmoid_f(a[k]);
+                const float silu = a[k] * sig;
+                x[i] = silu * v[k];
+                y[i] = g[k] * v[k] * (sig + silu * (1.0f - sig));
+                z[i] = g[k] * silu;
+              }
+              const __nv_bfloat162 xb = __floats2bfloat162_rn(x[0], x[1]);
+              const __nv_bfloat162 yb = __floats2bfloat162_rn(y[0], y[1]);
+              const __nv_bfloat162 zb = __floats2bfloat162_rn(z[0], z[1]);
+              h2[c] = *reinterpret_cast<const uint32_t*>(&xb);
+              da2[c] = *reinterpret_cast<const uint32_t*>(&yb);
+              du2[c] = *reinterpret_cast<const uint32_t*>(&zb);
             }
           }
-        } else {
-          float g[32];
-          ptx::tmem_ld32(tb + c0, g);
-          if (args.out_f32) {
-            float* o = static_cast<float*>(args.out) + obase;
+          if (last)
+            ctl.release(acc, lane);
+          else
+            fetch(q + 1);
+          if (!live) continue;
+          uint16_t* h = static_cast<uint16_t*>(args.out) + obase;
+          uint16_t* da = reinterpret_cast<uint16_t*>(args.da) + obase;
+          uint16_t* du = reinterpret_cast<uint16_t*>(args.du) + obase;
 #pragma unroll
-            for (int c = 0; c < 32; ++c)
-              if (col_ok && c0 + c < un.n_valid) o[(int64_t)(c0 + c) * args.cols] = g[c];
-          } else {
-            __nv_bfloat16* o = static_cast<__nv_bfloat16*>(args.out) + obase;
+          for (int c = 0; c < 32; ++c) {
+            const int r = 64 * q + r0 + c;
+            if (r < n_out) {
+              const int64_t at = (int64_t)r * args.cols;
+              h[at] = (uint16_t)((c & 1) ? h2[c >> 1] >> 16 : h2[c >> 1]);
+              da[at] = (uint16_t)((c & 1) ? da2[c >> 1] >> 16 : da2[c >> 1]);
+              du[at] = (uint16_t)((c & 1) ? du2[c >> 1] >> 16 : du2[c >> 1]);
+            }
+          }
+        }
+      } else {
+        // the whole share leaves TMEM before anything is stored, so the next
+        // unit's products wait for no store
+        constexpr int NQ = BN / 64, kPer = MODE == Mode::kDxF32 ? 32 : 16;
+        uint32_t w[NQ][kPer];
+        if (!full()) break;
 #pragma unroll
-            for (int c = 0; c < 32; ++c)
-              if (col_ok && c0 + c < un.n_valid)
-                o[(int64_t)(c0 + c) * args.cols] = __float2bfloat16_rn(g[c]);
+        for (int q = 0; q < NQ; ++q) {
+          if (64 * q + r0 < un.n_mma) {  // warp-uniform
+            float g[32];
+            ptx::tmem_ld32(tb + 64 * q, g);
+#pragma unroll
+            for (int c = 0; c < kPer; ++c) {
+              if (MODE == Mode::kDxF32) {
+                w[q][c] = __float_as_uint(g[c]);
+              } else {
+                const __nv_bfloat162 p = __floats2bfloat162_rn(g[2 * c], g[2 * c + 1]);
+                w[q][c] = *reinterpret_cast<const uint32_t*>(&p);
+              }
+            }
+          }
+        }
+        ctl.release(acc, lane);
+#pragma unroll
+        for (int q = 0; q < NQ; ++q) {
+          if (64 * q + r0 < un.n_mma) {
+#pragma unroll
+            for (int c = 0; c < 32; ++c) {
+              const int r = 64 * q + r0 + c;
+              if (r < n_out) {
+                const int64_t at = obase + (int64_t)r * args.cols;
+                if (MODE == Mode::kDxF32)
+                  static_cast<uint32_t*>(args.out)[at] = w[q][c % kPer];
+                else
+                  static_cast<uint16_t*>(args.out)[at] =
+                      (uint16_t)((c & 1) ? w[q][c / 2 % kPer] >> 16 : w[q][c / 2 % kPer]);
+              }
+            }
           }
         }
       }
-      ctl.release(acc, lane);
       if (++acc == C::kAccBufs) {
         acc = 0;
         acc_phase ^= 1u;
       }
     }
   }
-  ctl.finish(tmem_base);
+  ctl.finish(tmem_base, args.counters);
 }
 
 // -------------------------------------------------------- weight gradients --
+constexpr int kBoxes = 4;  // boxes of 64, 16, 8 and 4 rows, then single rows
 struct DwJob {
-  CUtensorMap a64, a16, a1;  // dy: 64-, 16- and 1-row boxes of 64 columns
-  CUtensorMap b64, b16, b1;  // x
-  CUtensorMap out;           // dw: 32 rows of 128 bytes
+  CUtensorMap a[kBoxes + 1];  // dy, 64 columns wide (a[0]: 2 x 64 if n_out is a
+                              // multiple of 64)
+  CUtensorMap b[kBoxes + 1];  // x
+  CUtensorMap out;            // dw: 32 rows of 128 bytes
   int n_out, n_in;
 };
 struct DwMaps {
@@ -572,62 +833,115 @@ struct DwMaps {
 struct DwArgs {
   const int32_t* offsets;
   int32_t* err;
+  int32_t* counters;  // two, zero between launches
   int64_t rows;
   int groups;
   int n_jobs;
-  bool out_f32;
 };
 
-// Tile: 128 rows of dw per CTA x 256 columns; TMEM holds two accumulators.
-template <bool PAIR_>
+// A CTA pair computes tiles of 256 x 256: each CTA has 128 rows of dw (its own
+// dy columns) and all 256 columns (half of the x columns in its own shared
+// memory); TMEM holds two accumulators. A unit is a run of up to kRun tiles of
+// one row of tiles. A segment of at most kASlots blocks of 64 rows keeps its dy
+// panel in shared memory for the whole run, so only x streams: half the
+// operand bytes of loading both, which is what bounds short segments (their
+// operands come from L2 at about 64 bytes a clock and SM).
 struct DwCfg {
-  static constexpr bool PAIR = PAIR_;
-  static constexpr int kCtas = PAIR ? 2 : 1;
-  static constexpr int BN = 256;
-  static constexpr int kABlocks = 2, kBBlocks = BN / 64 / kCtas;  // 64-column blocks per CTA
-  static constexpr uint32_t kStageBytes = (kABlocks + kBBlocks) * kBlockBytes;
-  static constexpr int kStages = PAIR ? 4 : 3;
-  static constexpr uint32_t kStageBuf = 4096;  // one warp's 32 rows x 128 bytes
-  static constexpr uint32_t kOutOff = kStages * kStageBytes;
-  static constexpr uint32_t kBarOff = kOutOff + kEpiWarps * 2 * kStageBuf;
-  static constexpr uint32_t kOffOff = kBarOff + 256;
+  static constexpr int kRun = 8;
+  static constexpr int kASlots = 6, kBSlots = 5;
+  static constexpr uint32_t kSlotBytes = 2 * kBlockBytes;  // 128 columns x 64 rows
+  static constexpr uint32_t kOutBuf = 4096;  // one warp's 32 rows x 128 bytes
+  static constexpr uint32_t kBOff = kASlots * kSlotBytes;
+  static constexpr uint32_t kOutOff = kBOff + kBSlots * kSlotBytes;
+  static constexpr uint32_t kBarOff = kOutOff + kEpiWarps * kOutBuf;
+  static constexpr uint32_t kOffOff = kBarOff + kCtlBytes;
   static constexpr uint32_t kSmemBytes = 1024 + kOffOff + 4 * (kMaxExperts + 1);
 };
 
 struct DwUnit {
-  int job, e, it, jt, row0, n_rows;
+  int job, e, it, jt0, jt1, row0, n_rows;
 };
 
-template <int CTAS>
+// Runs per row of tiles, of about equal length.
+__host__ __device__ __forceinline__ int dw_runs(int n_in) {
+  const int nj = (n_in + 255) / 256;
+  return (nj + DwCfg::kRun - 1) / DwCfg::kRun;
+}
+
 __device__ __forceinline__ DwUnit dw_unit(int u, const int* first, const DwMaps& maps,
                                           const int32_t* s_off) {
   DwUnit un;
   un.job = u >= first[2] ? 2 : (u >= first[1] ? 1 : 0);
   const DwJob& j = maps.job[un.job];
   const int v = u - first[un.job];
-  const int nj = (j.n_in + 255) / 256, ni = (j.n_out + BM * CTAS - 1) / (BM * CTAS);
-  un.jt = v % nj;
-  un.it = (v / nj) % ni;
-  un.e = v / nj / ni;
+  const int nj = (j.n_in + 255) / 256, ni = (j.n_out + 255) / 256, runs = dw_runs(j.n_in);
+  const int run = v % runs;
+  un.it = (v / runs) % ni;
+  un.e = v / runs / ni;
+  un.jt0 = nj * run / runs;
+  un.jt1 = nj * (run + 1) / runs;
   un.row0 = s_off[un.e];
   const int n = s_off[un.e + 1] - un.row0;
   un.n_rows = n > 0 ? n : 0;
   return un;
 }
 
-template <bool PAIR_>
+// 128 columns (from x) of the n rows from r0, rounded up to 16 rows, into two
+// 64-column blocks. Whole boxes where the rows are the segment's own; the last
+// one to three rows by gather4 with row `oob` (outside the tensor: zeros), and
+// boxes there for the rest of the 16.
+__device__ __forceinline__ void dw_load(const CUtensorMap* maps, bool wide, uint32_t dst,
+                                        uint32_t fb, int x, int r0, int n, int oob,
+                                        uint64_t pol) {
+  using G = Cg<true>;
+  if (wide && n == BK) {  // maps[0] is 3-D: both blocks in one copy
+    G::load_3d(maps, dst, fb, 0, r0, x / 64, pol);
+    return;
+  }
+#pragma unroll
+  for (int b = 0; b < 2; ++b) {
+    const int xb = x + 64 * b;
+    const uint32_t d = dst + b * kBlockBytes;
+    if (n == BK) {  // not wide
+      G::load_2d(maps, d, fb, xb, r0, pol);
+      continue;
+    }
+    int j = 0;
+    for (; j + 16 <= n; j += 16) G::load_2d(maps + 1, d + j * 128u, fb, xb, r0 + j, pol);
+    if (j + 8 <= n) {
+      G::load_2d(maps + 2, d + j * 128u, fb, xb, r0 + j, pol);
+      j += 8;
+    }
+    if (j + 4 <= n) {
+      G::load_2d(maps + 3, d + j * 128u, fb, xb, r0 + j, pol);
+      j += 4;
+    }
+    if (j < n) {
+      G::gather4(maps + 4, d + j * 128u, fb, xb, r0 + j, j + 1 < n ? r0 + j + 1 : oob,
+                 j + 2 < n ? r0 + j + 2 : oob, oob, pol);
+      j += 4;
+    }
+    if (j & 4) {
+      G::load_2d(maps + 3, d + j * 128u, fb, xb, oob, pol);
+      j += 4;
+    }
+    if (j & 8) G::load_2d(maps + 2, d + j * 128u, fb, xb, oob, pol);
+  }
+}
+
+template <bool OUT_F32>
 __global__ void __launch_bounds__(kThreads, 1)
     dw_gemm_kernel(const __grid_constant__ DwMaps maps, const DwArgs args) {
-  using C = DwCfg<PAIR_>;
-  using G = Cg<PAIR_>;
-  constexpr bool PAIR = PAIR_;
-  constexpr int S = C::kStages;
+  using C = DwCfg;
+  using G = Cg<true>;
+  constexpr int SA = C::kASlots, SB = C::kBSlots;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const uint32_t sbase = ptx::smem_addr(smem);
   int32_t* s_off = reinterpret_cast<int32_t*>(smem + C::kOffOff);
-  Control<S, PAIR> ctl;
+  // slots 0..SA-1 hold dy, SA..SA+SB-1 hold x; one pair of barriers each
+  Control<SA + SB, true> ctl;
   ctl.init(smem, sbase, C::kBarOff);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = G::rank();
@@ -648,187 +962,210 @@ __global__ void __launch_bounds__(kThreads, 1)
   for (int q = 0; q < kMaxJobs; ++q) {
     int n = 0;
     if (q < args.n_jobs)
-      n = args.groups * ((maps.job[q].n_out + BM * C::kCtas - 1) / (BM * C::kCtas)) *
-          ((maps.job[q].n_in + 255) / 256);
+      n = args.groups * ((maps.job[q].n_out + 255) / 256) * dw_runs(maps.job[q].n_in);
     first_unit[q + 1] = first_unit[q] + n;
   }
   const int total = first_unit[kMaxJobs];
-  const int first = (int)blockIdx.x / C::kCtas, stride = (int)gridDim.x / C::kCtas;
 
   if (warp == 0) {
     // ---------------------------------------------------- TMA producer --
-    if (lane == 0) {
-      const uint64_t pol = ptx::policy_evict_normal();
-      int stage = 0;
-      uint32_t phase = 0, armed = 0, armed_par = 0;
-      bool ok = true;
-      for (int u = first; u < total && ok; u += stride) {
-        const DwUnit un = dw_unit<C::kCtas>(u, first_unit, maps, s_off);
-        const DwJob& job = maps.job[un.job];
-        const int acol = (un.it * C::kCtas + (int)rank) * BM;
-        const int bcol = un.jt * 256 + (int)rank * (C::kBBlocks * 64);
+    const bool elected = elect_one();
+    const uint64_t pol = ptx::policy_evict_normal();
+    const uint32_t full0 = G::at_leader(ctl.full(0));
+    const int oob = (int)args.rows;
+    int sa = 0, sb = 0, claimed = 0;
+    uint32_t pa = 0, pb = 0, armed = 0, armed_par = 0;
+    bool ok = true;
+    // waits for a slot and fills it with 128 columns of rows r0 .. r0 + n - 1
+    auto fill = [&](int slot, uint32_t par, const CUtensorMap* m, bool wide, int x, int r0,
+                    int n) -> bool {
+      if (!wait_warp(ctl.empty(slot), par ^ 1u, ctl.abort_flag, args.err)) return false;
+      if (elected) {
+        if (rank == 0)
+          ptx::mbar_arrive_expect_tx(ctl.full(slot), 2u * 2u * 128u * (uint32_t)((n + 15) & ~15));
+        dw_load(m, wide, sbase + slot * C::kSlotBytes, full0 + 8u * slot, x, r0, n, oob, pol);
+      }
+      armed |= 1u << slot;
+      armed_par = (armed_par & ~(1u << slot)) | (par << slot);
+      return true;
+    };
+    for (int seq = 0, u; ok; ++seq) {
+      ok = ctl.next(seq, total, args.counters, &claimed, &u, args.err);
+      if (!ok || u < 0) break;
+      const DwUnit un = dw_unit(u, first_unit, maps, s_off);
+      const DwJob& job = maps.job[un.job];
+      const bool wide_a = job.n_out % 64 == 0, wide_b = job.n_in % 64 == 0;
+      const int acol = (un.it * 2 + (int)rank) * BM;
+      const bool keep = un.n_rows <= SA * BK;
+      for (int jt = un.jt0; jt < un.jt1 && ok; ++jt) {
+        const int bcol = jt * 256 + (int)rank * 128;
         for (int k0 = 0; k0 < un.n_rows; k0 += BK) {
-          if (!wait_bounded(ctl.empty(stage), phase ^ 1u, ctl.abort_flag, args.err)) {
-            ok = false;
-            break;
-          }
           const int left = un.n_rows - k0;
-          const int n = left < BK ? left : BK;       // rows of this block
-          const int n16 = (n + 15) & ~15;            // rows the MMAs read
-          if (rank == 0)
-            ptx::mbar_arrive_expect_tx(
-                ctl.full(stage),
-                (uint32_t)(C::kCtas * (C::kABlocks + C::kBBlocks)) * (uint32_t)n16 * 128u);
-          const uint32_t fb = G::at_leader(ctl.full(stage));
-          const uint32_t s0 = sbase + stage * C::kStageBytes;
-          const int r0 = un.row0 + k0;
-          const int oob = (int)args.rows;  // a row outside the tensors: zeros
-#pragma unroll
-          for (int b = 0; b < C::kABlocks + C::kBBlocks; ++b) {
-            const bool is_a = b < C::kABlocks;
-            const int x = is_a ? acol + 64 * b : bcol + 64 * (b - C::kABlocks);
-            const uint32_t dst = s0 + b * kBlockBytes;
-            if (n == BK) {
-              G::load_2d(is_a ? &job.a64 : &job.b64, dst, fb, x, r0, pol);
-            } else {
-              int j = 0;
-              for (; j + 16 <= n; j += 16)
-                G::load_2d(is_a ? &job.a16 : &job.b16, dst + j * 128u, fb, x, r0 + j, pol);
-              for (; j < n16; j += 4)
-                G::gather4(is_a ? &job.a1 : &job.b1, dst + j * 128u, fb, x,
-                           j < n ? r0 + j : oob, j + 1 < n ? r0 + j + 1 : oob,
-                           j + 2 < n ? r0 + j + 2 : oob, j + 3 < n ? r0 + j + 3 : oob, pol);
+          const int n = left < BK ? left : BK;
+          if (jt == un.jt0 || !keep) {
+            if (!(ok = fill(sa, pa, job.a, wide_a, acol, un.row0 + k0, n))) break;
+            if (++sa == SA) {
+              sa = 0;
+              pa ^= 1u;
             }
           }
-          armed |= 1u << stage;
-          armed_par = (armed_par & ~(1u << stage)) | (phase << stage);
-          if (++stage == S) {
-            stage = 0;
-            phase ^= 1u;
+          if (!(ok = fill(SA + sb, pb, job.b, wide_b, bcol, un.row0 + k0, n))) break;
+          if (++sb == SB) {
+            sb = 0;
+            pb ^= 1u;
           }
         }
       }
-      if (!ok) ctl.settle_loads(armed, armed_par);
     }
+    if (!ok && elected) ctl.settle_loads(armed, armed_par);
+    __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------ MMA issuer --
-    if (lane == 0 && rank == 0) {
-      const uint32_t idesc = ptx::idesc_bf16_f32(BM * C::kCtas, C::BN) | kAMn | kBMn;
-      int stage = 0, acc = 0;
-      uint32_t phase = 0, acc_phase = 0;
+    if (rank == 0) {
+      const bool elected = elect_one();
+      const uint64_t hi = desc_mn_sw128(0);
+      const uint32_t idesc = ptx::idesc_bf16_f32(256, 256) | kAMn | kBMn;
+      int sa = 0, sb = 0, acc = 0;
+      uint32_t pa = 0, pb = 0, acc_phase = 0;
       bool ok = true, issued = false;
-      for (int u = first; u < total && ok; u += stride) {
-        const DwUnit un = dw_unit<C::kCtas>(u, first_unit, maps, s_off);
+      for (int seq = 0, u; ok; ++seq) {
+        ok = ctl.take_warp(seq, &u, args.err);
+        if (!ok || u < 0) break;
+        const DwUnit un = dw_unit(u, first_unit, maps, s_off);
         if (un.n_rows == 0) continue;  // the epilogue writes zeros by itself
-        if (!wait_bounded(ctl.tempty(acc), acc_phase ^ 1u, ctl.abort_flag, args.err)) {
-          ok = false;
-          break;
-        }
-        ptx::tc_fence_after();
-        const uint32_t d0 = tmem_base + (uint32_t)acc * kAccStride;
-        for (int k0 = 0; k0 < un.n_rows; k0 += BK) {
-          if (!wait_bounded(ctl.full(stage), phase, ctl.abort_flag, args.err)) {
-            ok = false;
-            break;
-          }
+        const bool keep = un.n_rows <= SA * BK;
+        const int sa0 = sa;
+        const uint32_t pa0 = pa;
+        for (int jt = un.jt0; jt < un.jt1 && ok; ++jt) {
+          if (!(ok = wait_warp(ctl.tempty(acc), acc_phase ^ 1u, ctl.abort_flag, args.err))) break;
           ptx::tc_fence_after();
-          const int left = un.n_rows - k0;
-          const int steps = left >= BK ? BK / 16 : (left + 15) / 16;
-          const uint32_t a0 = sbase + stage * C::kStageBytes;
-          const uint32_t b0 = a0 + C::kABlocks * kBlockBytes;
-          for (int kk = 0; kk < steps; ++kk)
-            G::mma(d0, desc_mn_sw128(a0 + kk * 2048), desc_mn_sw128(b0 + kk * 2048), idesc,
-                   (k0 | kk) != 0 ? 1u : 0u);
-          issued = true;
-          G::commit(ctl.empty(stage));
-          if (++stage == S) {
-            stage = 0;
-            phase ^= 1u;
+          const uint32_t d0 = tmem_base + (uint32_t)acc * kAccStride;
+          const bool load_a = jt == un.jt0 || !keep;
+          const bool free_a = jt == un.jt1 - 1 || !keep;
+          if (keep) {  // each tile of the run reads the same slots
+            sa = sa0;
+            pa = pa0;
           }
-        }
-        if (!ok) break;
-        G::commit(ctl.tfull(acc));
-        if (++acc == 2) {
-          acc = 0;
-          acc_phase ^= 1u;
+          for (int k0 = 0; k0 < un.n_rows; k0 += BK) {
+            if (load_a && !(ok = wait_warp(ctl.full(sa), pa, ctl.abort_flag, args.err))) break;
+            if (!(ok = wait_warp(ctl.full(SA + sb), pb, ctl.abort_flag, args.err))) break;
+            ptx::tc_fence_after();
+            const int left = un.n_rows - k0;
+            if (elected) {
+              const uint64_t a = hi | ((sbase + sa * C::kSlotBytes) >> 4);
+              const uint64_t b = hi | ((sbase + C::kBOff + sb * C::kSlotBytes) >> 4);
+              if (left > BK - 16) {
+                mma_stage<true, 128, 128>(d0, a, b, idesc, k0 != 0 ? 1u : 0u);
+              } else {
+                for (int kk = 0; kk * 16 < left; ++kk)
+                  G::mma(d0, a + kk * 128, b + kk * 128, idesc, (k0 | kk) != 0 ? 1u : 0u);
+              }
+              G::commit(ctl.empty(SA + sb));
+              if (free_a) G::commit(ctl.empty(sa));
+            }
+            issued = true;
+            if (++sa == SA) {
+              sa = 0;
+              pa ^= 1u;
+            }
+            if (++sb == SB) {
+              sb = 0;
+              pb ^= 1u;
+            }
+          }
+          if (!ok) break;
+          if (elected) G::commit(ctl.tfull(acc));
+          if (++acc == 2) {
+            acc = 0;
+            acc_phase ^= 1u;
+          }
         }
       }
-      if (!ok && issued) {
+      if (!ok && issued && elected) {
         G::commit(ctl.mma_done());
         wait_cleanup(ctl.mma_done(), 0);
       }
+      __syncwarp();
     }
   } else {
     // -------------------------------------------------------- epilogue --
-    // A warp owns 32 rows (its TMEM lanes) and half of the 256 columns. Each
-    // 128-byte-wide piece (64 bf16 or 32 float columns) is laid out swizzled in
-    // shared memory and stored by TMA, which clips it to the matrix.
+    // A warp owns 32 rows (its TMEM lanes) and half of the 256 columns. It takes
+    // its whole share out of TMEM and hands the accumulator back before it
+    // stores anything. Each 128-byte-wide piece (64 bf16 or 32 float columns) is
+    // laid out swizzled in shared memory and stored by TMA, which clips it to
+    // the matrix.
     const int ew = warp & 3, eh = (warp - 2) >> 2;
-    const uint32_t buf0 = sbase + C::kOutOff + (uint32_t)(warp - 2) * 2 * C::kStageBuf;
-    int acc = 0, piece = 0;
+    const uint32_t buf = sbase + C::kOutOff + (uint32_t)(warp - 2) * C::kOutBuf;
+    constexpr int kWidth = OUT_F32 ? 32 : 64, kPieces = 128 / kWidth;
+    int acc = 0;
     uint32_t acc_phase = 0;
     bool ok = true;
-    for (int u = first; u < total && ok; u += stride) {
-      const DwUnit un = dw_unit<C::kCtas>(u, first_unit, maps, s_off);
+    for (int seq = 0, u; ok && ctl.take_warp(seq, &u, args.err) && u >= 0; ++seq) {
+      const DwUnit un = dw_unit(u, first_unit, maps, s_off);
       const DwJob& job = maps.job[un.job];
-      const bool some = un.n_rows > 0;
-      if (some) {
-        ok = __all_sync(0xffffffffu,
-                        wait_bounded(ctl.tfull(acc), acc_phase, ctl.abort_flag, args.err));
-        if (!ok) break;
-        ptx::tc_fence_after();
-      }
-      const uint32_t tb =
-          tmem_base + (static_cast<uint32_t>(ew * 32) << 16) + (uint32_t)acc * kAccStride;
-      const int row = (un.it * C::kCtas + (int)rank) * BM + ew * 32;
-      const int width = args.out_f32 ? 32 : 64;
-      const bool rows_in = row < job.n_out;
-      for (int c0 = eh * 128; c0 < eh * 128 + 128; c0 += width) {
-        const int col = un.jt * 256 + c0;
-        if (!rows_in || col >= job.n_in) continue;  // warp-uniform
-        const uint32_t buf = buf0 + (uint32_t)(piece & 1) * C::kStageBuf;
-        uint32_t w[32];
-        if (args.out_f32) {
-          float g[32];
-          if (some) ptx::tmem_ld32(tb + c0, g);
+      const int n_out = job.n_out, n_in = job.n_in;
+      const int row = (un.it * 2 + (int)rank) * BM + ew * 32;
+      for (int jt = un.jt0; jt < un.jt1; ++jt) {
+        uint32_t w[kPieces][32];
+        if (un.n_rows > 0) {
+          ok = __all_sync(0xffffffffu,
+                          wait_bounded(ctl.tfull(acc), acc_phase, ctl.abort_flag, args.err));
+          if (!ok) break;
+          ptx::tc_fence_after();
+          const uint32_t tb = tmem_base + (static_cast<uint32_t>(ew * 32) << 16) +
+                              (uint32_t)acc * kAccStride + (uint32_t)eh * 128u;
 #pragma unroll
-          for (int c = 0; c < 32; ++c) w[c] = some ? __float_as_uint(g[c]) : 0u;
-        } else {
-          float g[32], v[32];
-          if (some) ptx::tmem_ld32x2(tb + c0, tb + c0 + 32, g, v);
+          for (int q = 0; q < kPieces; ++q) {
+            float g[32];
+            if (OUT_F32) {
+              ptx::tmem_ld32(tb + 32 * q, g);
 #pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            const __nv_bfloat162 p = __floats2bfloat162_rn(g[2 * c], g[2 * c + 1]);
-            const __nv_bfloat162 q = __floats2bfloat162_rn(v[2 * c], v[2 * c + 1]);
-            w[c] = some ? *reinterpret_cast<const uint32_t*>(&p) : 0u;
-            w[16 + c] = some ? *reinterpret_cast<const uint32_t*>(&q) : 0u;
+              for (int c = 0; c < 32; ++c) w[q][c] = __float_as_uint(g[c]);
+            } else {
+              float v[32];
+              ptx::tmem_ld32x2(tb + 64 * q, tb + 64 * q + 32, g, v);
+#pragma unroll
+              for (int c = 0; c < 16; ++c) {
+                const __nv_bfloat162 lo = __floats2bfloat162_rn(g[2 * c], g[2 * c + 1]);
+                const __nv_bfloat162 hi = __floats2bfloat162_rn(v[2 * c], v[2 * c + 1]);
+                w[q][c] = *reinterpret_cast<const uint32_t*>(&lo);
+                w[q][16 + c] = *reinterpret_cast<const uint32_t*>(&hi);
+              }
+            }
           }
-        }
-        if (lane == 0) store_wait_read<1>();  // this buffer's last store has read it
-        __syncwarp();
+          ctl.release(acc, lane);
+          if (++acc == 2) {
+            acc = 0;
+            acc_phase ^= 1u;
+          }
+        } else {
 #pragma unroll
-        for (int c = 0; c < 8; ++c)
-          st_shared_v4(buf + lane * 128u + (uint32_t)((c ^ (lane & 7)) << 4), w[4 * c],
-                       w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          tma_store_3d(&job.out, buf, col, row, un.e);
-          store_commit();
+          for (int q = 0; q < kPieces; ++q)
+#pragma unroll
+            for (int c = 0; c < 32; ++c) w[q][c] = 0u;
         }
-        ++piece;
-      }
-      if (some) {
-        ctl.release(acc, lane);
-        if (++acc == 2) {
-          acc = 0;
-          acc_phase ^= 1u;
+#pragma unroll
+        for (int q = 0; q < kPieces; ++q) {
+          const int col = jt * 256 + eh * 128 + q * kWidth;
+          if (row >= n_out || col >= n_in) continue;  // warp-uniform
+          if (lane == 0) store_wait_read<0>();  // the last store has read the buffer
+          __syncwarp();
+#pragma unroll
+          for (int c = 0; c < 8; ++c)
+            st_shared_v4(buf + lane * 128u + (uint32_t)((c ^ (lane & 7)) << 4), w[q][4 * c],
+                         w[q][4 * c + 1], w[q][4 * c + 2], w[q][4 * c + 3]);
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_3d(&job.out, buf, col, row, un.e);
+            store_commit();
+          }
         }
       }
     }
     if (lane == 0) store_wait_all();
   }
-  ctl.finish(tmem_base);
+  ctl.finish(tmem_base, args.counters);
 }
 
 // -------------------------------------------------------------------- host --
@@ -846,21 +1183,18 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
 }
 
 bool encode(CUtensorMap* map, bool f32, int rank, const void* base, const uint64_t* dims,
-            const uint32_t* box) {
+            const uint64_t* strides, const uint32_t* box) {
   PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
   if (!enc) return false;
-  const uint64_t es = f32 ? 4 : 2;
-  cuuint64_t d[3], strides[2];
-  cuuint32_t b[3], one[3] = {1, 1, 1};
-  uint64_t bytes = es;
+  cuuint64_t d[4], st[4];
+  cuuint32_t b[4], one[4] = {1, 1, 1, 1};
   for (int i = 0; i < rank; ++i) {
     d[i] = dims[i];
     b[i] = box[i];
-    bytes *= dims[i];
-    if (i + 1 < rank) strides[i] = bytes;
+    if (i + 1 < rank) st[i] = strides[i];
   }
   return enc(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-             (cuuint32_t)rank, const_cast<void*>(base), d, strides, b, one,
+             (cuuint32_t)rank, const_cast<void*>(base), d, st, b, one,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -868,15 +1202,32 @@ bool encode(CUtensorMap* map, bool f32, int rank, const void* base, const uint64
 // Row-major bf16 [rows, cols], box of 64 columns x box_rows.
 bool rows_map(CUtensorMap* map, const void* base, int64_t rows, int cols, uint32_t box_rows) {
   const uint64_t dims[2] = {(uint64_t)cols, (uint64_t)rows};
+  const uint64_t strides[1] = {(uint64_t)cols * 2};
   const uint32_t box[2] = {64, box_rows};
-  return encode(map, false, 2, base, dims, box);
+  return encode(map, false, 2, base, dims, strides, box);
+}
+// The same as [cols / 64][rows][64], box of two 64-column blocks x 64 rows.
+bool wide_rows_map(CUtensorMap* map, const void* base, int64_t rows, int cols) {
+  const uint64_t dims[3] = {64, (uint64_t)rows, (uint64_t)cols / 64};
+  const uint64_t strides[2] = {(uint64_t)cols * 2, 128};
+  const uint32_t box[3] = {64, 64, 2};
+  return encode(map, false, 3, base, dims, strides, box);
 }
 // [groups, n_out, n_in], box of box_cols columns x box_rows rows of one group.
 bool group_map(CUtensorMap* map, bool f32, const void* base, int groups, int n_out, int n_in,
                uint32_t box_cols, uint32_t box_rows) {
+  const uint64_t es = f32 ? 4 : 2;
   const uint64_t dims[3] = {(uint64_t)n_in, (uint64_t)n_out, (uint64_t)groups};
+  const uint64_t strides[2] = {n_in * es, (uint64_t)n_out * n_in * es};
   const uint32_t box[3] = {box_cols, box_rows, 1};
-  return encode(map, f32, 3, base, dims, box);
+  return encode(map, f32, 3, base, dims, strides, box);
+}
+// The same as [groups][n_in / 64][n_out][64], box of two blocks x 64 rows.
+bool wide_group_map(CUtensorMap* map, const void* base, int groups, int n_out, int n_in) {
+  const uint64_t dims[4] = {64, (uint64_t)n_out, (uint64_t)n_in / 64, (uint64_t)groups};
+  const uint64_t strides[3] = {(uint64_t)n_in * 2, 128, (uint64_t)n_out * n_in * 2};
+  const uint32_t box[4] = {64, 64, 2, 1};
+  return encode(map, false, 4, base, dims, strides, box);
 }
 
 // Persistent launch: one CTA per SM, or as many pairs as can be resident.
@@ -940,6 +1291,14 @@ cudaError_t run_rows_sized(const RowMaps& maps, const RowArgs& args, cudaStream_
   return run_rows<MODE, 256, true>(maps, args, st);
 }
 
+template <bool OUT_F32>
+cudaError_t run_dw(const DwMaps& maps, const DwArgs& args, cudaStream_t st) {
+  static std::atomic<uint64_t> attr_set{0};
+  static std::atomic<int> grids[64];
+  return launch_persistent<true>(dw_gemm_kernel<OUT_F32>, DwCfg::kSmemBytes,
+                                 attr_set, grids, st, maps, args);
+}
+
 }  // namespace
 
 cudaError_t launch_grouped_rows_tc(const GroupedShape& g, const GroupedJob& job,
@@ -950,23 +1309,29 @@ cudaError_t launch_grouped_rows_tc(const GroupedShape& g, const GroupedJob& job,
   const void* w[2] = {job.b, job.b2 ? job.b2 : job.b};
   const void* r[2] = {job.a, job.a2 ? job.a2 : job.a};
   bool ok = true;
-  for (int q = 0; q < 2; ++q)
-    ok = ok && group_map(&maps.w[q], false, w[q], g.groups, job.n_out, job.n_in, 64,
-                         fwd ? 128 : 64) &&
-         rows_map(&maps.r16[q], r[q], g.rows, k, 16) &&
-         rows_map(&maps.r128[q], r[q], g.rows, k, 128);
+  const bool wide = !fwd && job.n_in % 64 == 0;
+  for (int q = 0; q < 2; ++q) {
+    ok = ok && (wide ? wide_group_map(&maps.w[q], w[q], g.groups, job.n_out, job.n_in)
+                     : group_map(&maps.w[q], false, w[q], g.groups, job.n_out, job.n_in, 64,
+                                 fwd ? 128 : 64));
+    for (int i = 0; i < kRowBoxes; ++i)
+      ok = ok && rows_map(&maps.r[q][i], r[q], g.rows, k, 128u >> i);
+  }
   if (!ok) return cudaErrorInvalidValue;
   RowArgs a = {};
   a.offsets = offsets;
   a.err = err;
+  a.counters = err + kUnitCounter;
   a.rows = g.rows;
   a.groups = g.groups;
   a.cols = fwd ? job.n_out : job.n_in;
   a.k_blocks = (k + BK - 1) / BK;
+  a.wide_w = wide;
   a.sources = job.a2 ? 2 : 1;
   a.out = job.out;
-  a.out_f32 = job.out_f32;
-  return fwd ? run_rows_sized<Mode::kFwd>(maps, a, st) : run_rows_sized<Mode::kDx>(maps, a, st);
+  if (fwd) return run_rows_sized<Mode::kFwd>(maps, a, st);
+  return job.out_f32 ? run_rows_sized<Mode::kDxF32>(maps, a, st)
+                     : run_rows_sized<Mode::kDx>(maps, a, st);
 }
 
 cudaError_t launch_swiglu_backward_tc(const GroupedShape& g, const void* x, const void* w_gate,
@@ -976,13 +1341,16 @@ cudaError_t launch_swiglu_backward_tc(const GroupedShape& g, const void* x, cons
   RowMaps maps;
   const void* w[2] = {w_gate, w_up};
   bool ok = true;
-  for (int q = 0; q < 2; ++q)
-    ok = ok && group_map(&maps.w[q], false, w[q], g.groups, F, d, 64, 128) &&
-         rows_map(&maps.r16[q], x, g.rows, d, 16) && rows_map(&maps.r128[q], x, g.rows, d, 128);
+  for (int q = 0; q < 2; ++q) {
+    ok = ok && group_map(&maps.w[q], false, w[q], g.groups, F, d, 64, 128);
+    for (int i = 0; i < kRowBoxes; ++i)
+      ok = ok && rows_map(&maps.r[q][i], x, g.rows, d, 128u >> i);
+  }
   if (!ok) return cudaErrorInvalidValue;
   RowArgs a = {};
   a.offsets = offsets;
   a.err = err;
+  a.counters = err + kUnitCounter;
   a.rows = g.rows;
   a.groups = g.groups;
   a.cols = F;
@@ -1003,27 +1371,25 @@ cudaError_t launch_grouped_dw_tc(const GroupedShape& g, const GroupedJob* jobs, 
     DwJob& m = maps.job[q];
     m.n_out = j.n_out;
     m.n_in = j.n_in;
-    const bool ok = rows_map(&m.a64, j.a, g.rows, j.n_out, 64) &&
-                    rows_map(&m.a16, j.a, g.rows, j.n_out, 16) &&
-                    rows_map(&m.a1, j.a, g.rows, j.n_out, 1) &&
-                    rows_map(&m.b64, j.b, g.rows, j.n_in, 64) &&
-                    rows_map(&m.b16, j.b, g.rows, j.n_in, 16) &&
-                    rows_map(&m.b1, j.b, g.rows, j.n_in, 1) &&
-                    group_map(&m.out, j.out_f32, j.out, g.groups, j.n_out, j.n_in,
-                              j.out_f32 ? 32 : 64, 32);
+    const uint32_t box[kBoxes + 1] = {64, 16, 8, 4, 1};
+    bool ok = group_map(&m.out, j.out_f32, j.out, g.groups, j.n_out, j.n_in,
+                        j.out_f32 ? 32 : 64, 32);
+    for (int i = 0; i <= kBoxes; ++i)
+      ok = ok &&
+           (i == 0 && j.n_out % 64 == 0 ? wide_rows_map(&m.a[i], j.a, g.rows, j.n_out)
+                                        : rows_map(&m.a[i], j.a, g.rows, j.n_out, box[i])) &&
+           (i == 0 && j.n_in % 64 == 0 ? wide_rows_map(&m.b[i], j.b, g.rows, j.n_in)
+                                       : rows_map(&m.b[i], j.b, g.rows, j.n_in, box[i]));
     if (!ok) return cudaErrorInvalidValue;
   }
   DwArgs a = {};
   a.offsets = offsets;
   a.err = err;
+  a.counters = err + kUnitCounter;
   a.rows = g.rows;
   a.groups = g.groups;
   a.n_jobs = n_jobs;
-  a.out_f32 = jobs[0].out_f32;
-  static std::atomic<uint64_t> attr_set{0};
-  static std::atomic<int> grids[64];
-  return launch_persistent<true>(dw_gemm_kernel<true>, DwCfg<true>::kSmemBytes, attr_set, grids,
-                                 st, maps, a);
+  return jobs[0].out_f32 ? run_dw<true>(maps, a, st) : run_dw<false>(maps, a, st);
 }
 
 }  // namespace moe

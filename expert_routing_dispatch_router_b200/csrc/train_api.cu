@@ -44,7 +44,7 @@ bool disjoint(const Span (&s)[N]) {
 
 moe_status_t cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
 
-constexpr size_t kGroupedWs = 256;  // the error word
+constexpr size_t kGroupedWs = 256;  // the error word and unit counters
 
 moe_status_t grouped_check(const moe_grouped_t* c) {
   if (c == nullptr) return MOE_ERR_INVALID_ARG;

@@ -306,8 +306,9 @@ moe_status_t moe_bias_pid_update(const moe_config_t* cfg, const int32_t* counts,
  *  Limits: 1 <= groups <= 1024, n_in and n_out multiples of 8, and
  *  (rows / 64 + groups) * (max(n_in, n_out) / 64 + 1) and
  *  groups * (n_in / 64 + 1) * (n_out / 64 + 1) below 2^31.
- *  The workspace is one error word: moe_grouped_workspace_size bytes, 256-byte
- *  aligned, zero before first use, read with moe_read_device_error. */
+ *  The workspace holds the error word and small counters that the kernels
+ *  return to zero: moe_grouped_workspace_size bytes, 256-byte aligned, zero
+ *  before first use, ordered on one stream, read with moe_read_device_error. */
 typedef struct {
   int32_t rows;
   int32_t groups;
