@@ -44,25 +44,29 @@ struct GroupedShape {
 // error word (bounded waits of the tensor-core kernels).
 cudaError_t launch_grouped_jobs(const GroupedShape& g, const GroupedJob* jobs, int n_jobs,
                                 const int32_t* offsets, int32_t* err, cudaStream_t st);
-// Its tensor-core parts, and the gate/up product whose epilogue is the SwiGLU
-// backward: from dh (float) it leaves h, da and du.
+// Its tensor-core parts, and the first half of the experts' backward pass: from
+// x, dy and the weights to h, da and du, with the pre-activations in float on
+// the way.
 cudaError_t launch_grouped_rows_tc(const GroupedShape& g, const GroupedJob& job,
                                    const int32_t* offsets, int32_t* err, cudaStream_t st);
 cudaError_t launch_grouped_dw_tc(const GroupedShape& g, const GroupedJob* jobs, int n_jobs,
                                  const int32_t* offsets, int32_t* err, cudaStream_t st);
 cudaError_t launch_swiglu_backward_tc(const GroupedShape& g, const void* x, const void* w_gate,
-                                      const void* w_up, const float* dh, void* h, void* da,
-                                      void* du, int d, int F, const int32_t* offsets,
-                                      int32_t* err, cudaStream_t st);
+                                      const void* w_up, const void* dy, const void* w_down,
+                                      float* pre_a, float* pre_u, void* h, void* da, void* du,
+                                      int d, int F, const int32_t* offsets, int32_t* err,
+                                      cudaStream_t st);
 // Whether unit numbers of a product fit the kernels' 32-bit counters.
 bool grouped_fits(int64_t rows, int64_t groups, int64_t n_in, int64_t n_out);
 
 // ---- the experts' backward pass and the layer's other gradients ----
 struct BackwardWs {   // byte offsets from the workspace's base
   size_t header;      // int32[64]: [0] error code
-  size_t dh;          // float [T*k, F]: gradient of h
-  size_t h, da, du;   // act [T*k, F]: h and the gradients of the pre-activations
-                      // (float layers: da and du first hold those themselves)
+  size_t pre_a, pre_u;  // float [T*k, F]: the pre-activations (float layers:
+                        // then their gradients da and du)
+  size_t dh;          // float [T*k, F]: gradient of h (float layers)
+  size_t h;           // act [T*k, F]
+  size_t da, du;      // bf16 [T*k, F]: the pre-activations' gradients (bf16 layers)
   size_t dy_perm;     // act [T*k, d]  (whole-layer call)
   size_t dx_perm;     // act [T*k, d]  (whole-layer call)
   size_t dgate;       // float [T, k]  (whole-layer call)
@@ -96,13 +100,18 @@ cudaError_t launch_input_backward(const Shape& sh, const void* dout, const void*
 
 // ---- device helpers ----
 // Segment table of a block in shared memory: s_off[0..n] the row offsets,
-// s_tile[0..n] the prefix sums of ceil(rows / tile). Offsets are clamped to
+// s_tile[0..n] the prefix sums of the segments' tiles of `tile` rows, where up
+// to `slack` rows behind the last full tile count as part of it. Offsets are clamped to
 // [0, rows] and to be non-decreasing, so no table sends a kernel outside its
 // buffers. All THREADS threads call it; s_warp holds 32 ints. Each thread
 // takes `per` consecutive segments.
+__device__ __forceinline__ int32_t segment_tiles(int32_t rows, int tile, int slack) {
+  if (rows <= 0) return 0;
+  return rows <= tile + slack ? 1 : (rows - slack + tile - 1) / tile;
+}
 template <int THREADS>
 __device__ __forceinline__ void segment_table(const int32_t* __restrict__ offsets, int n,
-                                              int64_t rows, int tile, int32_t* s_off,
+                                              int64_t rows, int tile, int slack, int32_t* s_off,
                                               int32_t* s_tile, int32_t* s_warp) {
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   const int per = (n + THREADS - 1) / THREADS;
@@ -114,10 +123,7 @@ __device__ __forceinline__ void segment_table(const int32_t* __restrict__ offset
   int32_t sum = 0;
   for (int q = 0; q < per; ++q) {
     const int e = threadIdx.x * per + q;
-    if (e < n) {
-      const int32_t c = s_off[e + 1] - s_off[e];
-      sum += c > 0 ? (c + tile - 1) / tile : 0;
-    }
+    if (e < n) sum += segment_tiles(s_off[e + 1] - s_off[e], tile, slack);
   }
   int32_t incl = sum;
 #pragma unroll
@@ -133,8 +139,7 @@ __device__ __forceinline__ void segment_table(const int32_t* __restrict__ offset
     const int e = threadIdx.x * per + q;
     if (e < n) {
       s_tile[e] = before;
-      const int32_t c = s_off[e + 1] - s_off[e];
-      before += c > 0 ? (c + tile - 1) / tile : 0;
+      before += segment_tiles(s_off[e + 1] - s_off[e], tile, slack);
       if (e == n - 1) s_tile[n] = before;
     }
   }

@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(kSimtThreads)
   __shared__ int32_t s_off[kMaxExperts + 1], s_tile[kMaxExperts + 1], s_warp[32];
   griddep_wait();
   griddep_launch_dependents();
-  segment_table<kSimtThreads>(args.offsets, args.groups, args.rows, kTile, s_off, s_tile,
+  segment_table<kSimtThreads>(args.offsets, args.groups, args.rows, kTile, 0, s_off, s_tile,
                               s_warp);
   int64_t first[kMaxJobs + 1];
   first[0] = 0;

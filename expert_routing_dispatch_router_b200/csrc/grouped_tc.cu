@@ -12,8 +12,13 @@
 //   dx = dy W    contraction over n_out: W is read as it lies and its tile is
 //                MN-major (the output direction is contiguous); a second pair
 //                (dy2, W2) may extend the contraction
-//   the SwiGLU backward: gate and up accumulators of the same tile, and an
-//                epilogue that turns them and dh into h, da and du
+//   the experts' backward takes the pre-activations a = x W_gate^T and
+//                u = x W_up^T in float (one launch), and then dh = dy W_down with
+//                an epilogue that turns it, a and u into h, da and du
+// On CTA pairs a segment's last rows, up to kMerge of them behind a full tile of
+// 256, join that tile as a second MMA into the second accumulator: a unit of
+// their own would load the weight tile again, and operands from L2 (about 75
+// GB/s per SM) bound it.
 // Weight gradients (dw_gemm_kernel), dw[e] = dy^T x: contraction over the
 // segment's rows, both operands MN-major as they lie. The last rows of a
 // segment come by gather4 in groups of four, with a row outside the tensor
@@ -460,8 +465,13 @@ struct Control {
 };
 
 // ------------------------------------------------------------ row products --
-enum class Mode : int { kFwd, kDx, kDxF32, kGateUp };
-__host__ __device__ constexpr bool is_dx(Mode m) { return m == Mode::kDx || m == Mode::kDxF32; }
+enum class Mode : int {
+  kFwd,     // y, bf16
+  kFwdF32,  // two weights for the same rows, float: a and u
+  kDx,      // dx, bf16
+  kSwiglu   // dh, turned into h, da and du
+};
+__host__ __device__ constexpr bool is_dx(Mode m) { return m == Mode::kDx || m == Mode::kSwiglu; }
 
 struct RowArgs {
   const int32_t* offsets;
@@ -473,41 +483,40 @@ struct RowArgs {
   int k_blocks;  // per source
   bool wide_w;   // kDx: both 64-column blocks of a weight tile come in one copy
   int sources;   // 2: a second (weights, rows) pair extends the contraction
-  void* out;     // bf16 rows (kDxF32: float; kGateUp: h)
-  // kGateUp only
-  const float* dh;
-  __nv_bfloat16* da;
-  __nv_bfloat16* du;
+  // kFwd, kDx: out[0] bf16. kFwdF32: out[0] a, out[1] u. kSwiglu: out[0] h,
+  // out[1] da, out[2] du, all bf16, from pre[0] a and pre[1] u.
+  void* out[3];
+  const float* pre[2];
 };
 
 constexpr int kRowBoxes = 4;  // boxes of 128, 64, 32 and 16 rows
 struct RowMaps {
-  CUtensorMap w[2];  // weights (kGateUp: gate, up; kDx: the two sources)
+  CUtensorMap w[2];  // weights (kFwdF32: gate, up; kDx: the two sources)
   CUtensorMap r[2][kRowBoxes];
 };
 
-template <Mode MODE, int BN_, bool PAIR_>
+template <int BN_, bool PAIR_>
 struct RowCfg {
   static constexpr bool PAIR = PAIR_;
   static constexpr int kCtas = PAIR ? 2 : 1;
-  static constexpr int BN = BN_;
-  static constexpr int BNH = BN / kCtas;  // rows one CTA loads
-  static constexpr int kNumA = MODE == Mode::kGateUp ? 2 : 1;
+  static constexpr int BN = BN_;                    // rows of a tile
+  static constexpr int kMerge = PAIR ? 64 : 0;      // rows that may join the last one
+  static constexpr int BNH = BN / kCtas;            // rows one CTA loads, and of those
+  static constexpr int kMergeH = kMerge / kCtas;    // that join
   static_assert(BNH <= 128 && BN % (16 * kCtas) == 0, "rows of a unit");
-  static constexpr uint32_t kAccCols = kNumA * BN;
-  static constexpr int kAccBufs = kAccCols <= kAccStride ? 2 : 1;
-  static constexpr uint32_t kStageBytes = kNumA * kTileBytes + BNH * BK * 2;
-  static constexpr int kStages = 204800 / kStageBytes > 8 ? 8 : (int)(204800 / kStageBytes);
+  static constexpr uint32_t kStageBytes = kTileBytes + (BNH + kMergeH) * BK * 2;
+  static constexpr int kStages = 221184 / kStageBytes > 8 ? 8 : (int)(221184 / kStageBytes);
   static constexpr uint32_t kBarOff = kStages * kStageBytes;
   static constexpr uint32_t kTabOff = kBarOff + kCtlBytes;
   static constexpr uint32_t kSmemBytes = 1024 + kTabOff + 2 * 4 * (kMaxExperts + 1) + 128;
+  static_assert(kSmemBytes <= 232448, "shared memory of a CTA");
 };
 
 struct RowUnit {
-  int e, m, row0, n_valid, n_mma, ntiles;
+  int e, m, row0, n, ntiles;  // n rows: the first BN, then those that join them
 };
 
-template <int BN, int STEP>
+template <int BN>
 __device__ __forceinline__ RowUnit row_unit(int u, const int32_t* s_tile, const int32_t* s_off,
                                             int groups, int m_tiles) {
   int lo = 0, hi = groups - 1;  // largest e with m_tiles * s_tile[e] <= u
@@ -525,9 +534,7 @@ __device__ __forceinline__ RowUnit row_unit(int u, const int32_t* s_tile, const 
   un.m = local / un.ntiles;
   const int tt = local - un.m * un.ntiles;
   un.row0 = s_off[lo] + tt * BN;
-  const int rem = s_off[lo + 1] - un.row0;
-  un.n_valid = rem < BN ? rem : BN;
-  un.n_mma = (un.n_valid + STEP - 1) / STEP * STEP;
+  un.n = tt + 1 < un.ntiles ? BN : s_off[lo + 1] - un.row0;
   return un;
 }
 
@@ -541,7 +548,7 @@ __device__ __forceinline__ float sigmoid_f(float z) {
 template <Mode MODE, int BN_, bool PAIR_>
 __global__ void __launch_bounds__(kThreads, 1)
     row_gemm_kernel(const __grid_constant__ RowMaps maps, const RowArgs args) {
-  using C = RowCfg<MODE, BN_, PAIR_>;
+  using C = RowCfg<BN_, PAIR_>;
   using G = Cg<PAIR_>;
   constexpr bool PAIR = PAIR_;
   constexpr int S = C::kStages, BN = C::BN, STEP = 16 * C::kCtas;
@@ -564,15 +571,24 @@ __global__ void __launch_bounds__(kThreads, 1)
   // everything above overlaps the previous kernel's tail
   griddep_wait();
   griddep_launch_dependents();
-  segment_table<kThreads>(args.offsets, args.groups, args.rows, BN, s_off, s_tile, s_warp);
+  segment_table<kThreads>(args.offsets, args.groups, args.rows, BN, C::kMerge, s_off, s_tile,
+                          s_warp);
   ptx::tc_fence_before();
   __syncthreads();
   G::sync_all();  // both CTAs' barriers exist before any remote arrive
   ptx::tc_fence_after();
   const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(ctl.tmem_slot);
-  const int m_tiles = (args.cols + BM * C::kCtas - 1) / (BM * C::kCtas);
+  // column tiles of one weight matrix, and of a unit row (kFwdF32: gate's, then
+  // up's)
+  const int tiles = (args.cols + BM * C::kCtas - 1) / (BM * C::kCtas);
+  const int m_tiles = MODE == Mode::kFwdF32 ? 2 * tiles : tiles;
   const int total = s_tile[args.groups] * m_tiles;
   const int n_kb = args.k_blocks * args.sources;
+  // rows of a unit's two MMAs, rounded up to what an MMA takes
+  auto mma_rows = [](int n, int q) -> int {
+    const int r = q == 0 ? (n < BN ? n : BN) : n - BN;
+    return r > 0 ? (r + STEP - 1) / STEP * STEP : 0;
+  };
 
   if (warp == 0) {
     // ---------------------------------------------------- TMA producer --
@@ -587,11 +603,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int seq = 0, u; ok; ++seq) {
       ok = ctl.next(seq, total, args.counters, &claimed, &u, args.err);
       if (!ok || u < 0) break;
-      const RowUnit un = row_unit<BN, STEP>(u, s_tile, s_off, args.groups, m_tiles);
-      const int half = un.n_mma / C::kCtas;
-      const int col0 = (un.m * C::kCtas + (int)rank) * BM;
+      const RowUnit un = row_unit<BN>(u, s_tile, s_off, args.groups, m_tiles);
+      const int half = mma_rows(un.n, 0) / C::kCtas;
+      const int more = PAIR ? mma_rows(un.n, 1) / C::kCtas : 0;
+      const int job = MODE == Mode::kFwdF32 && un.m >= tiles ? 1 : 0;
+      const int col0 = ((un.m - job * tiles) * C::kCtas + (int)rank) * BM;
       const int brow = un.row0 + (int)rank * half;
-      const uint32_t bytes = (uint32_t)C::kCtas * (C::kNumA * kTileBytes + (uint32_t)half * 128u);
+      const uint32_t bytes = (uint32_t)C::kCtas * (kTileBytes + (uint32_t)(half + more) * 128u);
       // weights that only this unit reads (one row tile) are streamed
       const uint64_t pol_w = un.ntiles == 1 ? pol_first : pol_normal;
       for (int kb = 0; kb < n_kb; ++kb) {
@@ -603,16 +621,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t fb = full0 + 8u * stage;
           const uint32_t a0 = sbase + stage * C::kStageBytes;
           if (!is_dx(MODE)) {
-            G::load_3d(&maps.w[0], a0, fb, k0, col0, un.e, pol_w);
-            if (MODE == Mode::kGateUp)
-              G::load_3d(&maps.w[1], a0 + kTileBytes, fb, k0, col0, un.e, pol_w);
+            G::load_3d(&maps.w[job], a0, fb, k0, col0, un.e, pol_w);
           } else if (args.wide_w) {
             G::load_4d(&maps.w[src], a0, fb, 0, k0, col0 / 64, un.e, pol_w);
           } else {
             G::load_3d(&maps.w[src], a0, fb, col0, k0, un.e, pol_w);
             G::load_3d(&maps.w[src], a0 + kBlockBytes, fb, col0 + 64, k0, un.e, pol_w);
           }
-          uint32_t b0 = a0 + C::kNumA * kTileBytes;
+          uint32_t b0 = a0 + kTileBytes;
           int j = brow;
 #pragma unroll
           for (int q = 0; q < kRowBoxes; ++q) {
@@ -623,6 +639,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               j += h;
             }
           }
+          if (PAIR && more > 0)  // 16 or 32 rows
+            G::load_2d(&maps.r[src][more == 32 ? 2 : 3], a0 + kTileBytes + C::BNH * 128u, fb, k0,
+                       un.row0 + BN + (int)rank * more, pol_normal);
         }
         armed |= 1u << stage;
         armed_par = (armed_par & ~(1u << stage)) | (phase << stage);
@@ -636,34 +655,43 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------ MMA issuer --
-    // The warp stays converged and one lane issues.
+    // Accumulators alternate: MMA number `slot` (a unit has one or two) uses
+    // accumulator slot & 1.
     if (rank == 0) {
       const bool elected = elect_one();
       const uint64_t hi_k = ptx::desc_k_sw128(0), hi_mn = desc_mn_sw128(0);
-      constexpr uint32_t kAStep = is_dx(MODE) ? 2048 / 16 : 32 / 16;
-      int stage = 0, acc = 0;
-      uint32_t phase = 0, acc_phase = 0;
+      constexpr int kAStep = is_dx(MODE) ? 2048 / 16 : 32 / 16;
+      constexpr uint32_t kFlags = is_dx(MODE) ? kAMn : 0u;
+      int stage = 0;
+      uint32_t phase = 0, slot = 0;
       bool ok = true, issued = false;
       for (int seq = 0, u; ok; ++seq) {
         ok = ctl.take_warp(seq, &u, args.err);
         if (!ok || u < 0) break;
-        const RowUnit un = row_unit<BN, STEP>(u, s_tile, s_off, args.groups, m_tiles);
-        if (!(ok = wait_warp(ctl.tempty(acc), acc_phase ^ 1u, ctl.abort_flag, args.err))) break;
+        const RowUnit un = row_unit<BN>(u, s_tile, s_off, args.groups, m_tiles);
+        const int n0 = mma_rows(un.n, 0), n1 = PAIR ? mma_rows(un.n, 1) : 0;
+        if (!(ok = wait_warp(ctl.tempty(slot & 1), ((slot >> 1) & 1u) ^ 1u, ctl.abort_flag,
+                             args.err)))
+          break;
+        if (n1 > 0 && !(ok = wait_warp(ctl.tempty((slot + 1) & 1), (((slot + 1) >> 1) & 1u) ^ 1u,
+                                       ctl.abort_flag, args.err)))
+          break;
         ptx::tc_fence_after();
-        const uint32_t idesc = ptx::idesc_bf16_f32(BM * C::kCtas, un.n_mma) |
-                               (is_dx(MODE) ? kAMn : 0u);
-        const uint32_t d0 = tmem_base + (uint32_t)acc * kAccStride;
+        const uint32_t i0 = ptx::idesc_bf16_f32(BM * C::kCtas, n0) | kFlags;
+        const uint32_t i1 = ptx::idesc_bf16_f32(BM * C::kCtas, n1) | kFlags;
+        const uint32_t d0 = tmem_base + (slot & 1) * kAccStride;
+        const uint32_t d1 = tmem_base + ((slot + 1) & 1) * kAccStride;
         for (int kb = 0; kb < n_kb; ++kb) {
           if (!(ok = wait_warp(ctl.full(stage), phase, ctl.abort_flag, args.err))) break;
           ptx::tc_fence_after();
           if (elected) {
-            const uint64_t a = (is_dx(MODE) ? hi_mn : hi_k) | ((sbase + stage * C::kStageBytes) >> 4);
-            const uint64_t b =
-                hi_k | ((sbase + stage * C::kStageBytes + C::kNumA * kTileBytes) >> 4);
-            mma_stage<PAIR, kAStep, 2>(d0, a, b, idesc, kb != 0 ? 1u : 0u);
-            if (MODE == Mode::kGateUp)
-              mma_stage<PAIR, kAStep, 2>(d0 + BN, a + (kTileBytes >> 4), b, idesc,
-                                         kb != 0 ? 1u : 0u);
+            const uint32_t a0 = sbase + stage * C::kStageBytes;
+            const uint64_t a = (is_dx(MODE) ? hi_mn : hi_k) | (a0 >> 4);
+            const uint64_t b = hi_k | ((a0 + kTileBytes) >> 4);
+            const uint32_t accum = kb != 0 ? 1u : 0u;
+            mma_stage<PAIR, kAStep, 2>(d0, a, b, i0, accum);
+            if (PAIR && n1 > 0)
+              mma_stage<PAIR, kAStep, 2>(d1, a, b + (C::BNH * 128 >> 4), i1, accum);
             G::commit(ctl.empty(stage));
           }
           issued = true;
@@ -673,11 +701,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (!ok) break;
-        if (elected) G::commit(ctl.tfull(acc));
-        if (++acc == C::kAccBufs) {
-          acc = 0;
-          acc_phase ^= 1u;
+        if (elected) {
+          G::commit(ctl.tfull(slot & 1));
+          if (n1 > 0) G::commit(ctl.tfull((slot + 1) & 1));
         }
+        slot += n1 > 0 ? 2 : 1;
       }
       if (!ok && issued && elected) {  // MMAs already issued finish before TMEM is freed
         G::commit(ctl.mma_done());
@@ -688,58 +716,65 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     // -------------------------------------------------------- epilogue --
     const int ew = warp & 3;         // TMEM lane quarter this warp may access
-    const int eh = (warp - 2) >> 2;  // which half of the column chunks
-    int acc = 0;
-    uint32_t acc_phase = 0;
-    for (int seq = 0, u; ctl.take_warp(seq, &u, args.err) && u >= 0; ++seq) {
-      const RowUnit un = row_unit<BN, STEP>(u, s_tile, s_off, args.groups, m_tiles);
-      const int col = (un.m * C::kCtas + (int)rank) * BM + ew * 32 + lane;
-      const int64_t obase = (int64_t)un.row0 * args.cols + col;
-      const int n_out = col < args.cols ? un.n_valid : 0;  // rows this lane stores
-      auto full = [&]() -> bool {
-        const bool ok = wait_bounded(ctl.tfull(acc), acc_phase, ctl.abort_flag, args.err);
-        if (!__all_sync(0xffffffffu, ok)) return false;
-        ptx::tc_fence_after();
-        return true;
-      };
-      const uint32_t tb = tmem_base + (static_cast<uint32_t>(ew * 32) << 16) +
-                          (uint32_t)acc * kAccStride + 32u * eh;
-      // 32-row chunks, alternating between the two warps of this quarter: chunk
-      // q covers rows 64 q + 32 eh ..
-      const int r0 = 32 * eh;
-      if (MODE == Mode::kGateUp) {
-        // dh of a chunk is fetched ahead: the first while the unit's products
-        // still run, the others before the previous chunk's stores. The
-        // accumulator goes back as soon as the last chunk has left TMEM.
-        float g[32];
-        auto fetch = [&](int q) {
+    const int eh = (warp - 2) >> 2;  // which half of the 32-row chunks
+    uint32_t next_slot = 0;
+    bool ok = true;
+    for (int seq = 0, u; ok && ctl.take_warp(seq, &u, args.err) && u >= 0; ++seq) {
+      const RowUnit un = row_unit<BN>(u, s_tile, s_off, args.groups, m_tiles);
+      const int job = MODE == Mode::kFwdF32 && un.m >= tiles ? 1 : 0;
+      const int col = ((un.m - job * tiles) * C::kCtas + (int)rank) * BM + ew * 32 + lane;
+      const int parts = PAIR && un.n > BN ? 2 : 1;
+      // the rows that joined come first: they are few, and the next unit's
+      // products wait for both accumulators
+      for (int part = parts - 1; part >= 0; --part) {
+        const uint32_t slot = next_slot + part;
+        const int64_t obase = (int64_t)(un.row0 + part * BN) * args.cols + col;
+        const int n_rows = part == 0 ? (un.n < BN ? un.n : BN) : un.n - BN;
+        const int n_out = col < args.cols ? n_rows : 0;  // rows this lane stores
+        // 32-row chunks, alternating between the two warps of this quarter:
+        // chunk q covers rows 64 q + r0 ..
+        const int r0 = 32 * eh;
+        const uint32_t tb = tmem_base + (static_cast<uint32_t>(ew * 32) << 16) +
+                            (slot & 1) * kAccStride + (uint32_t)r0;
+        // kSwiglu takes half chunks of 16 rows (i -> row half_row(i)), whose
+        // pre-activations are fetched one ahead
+        auto half_row = [&](int i) { return 64 * (i >> 1) + r0 + 16 * (i & 1); };
+        float a[16], v[16];
+        auto fetch = [&](int i) {
 #pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            const int r = 64 * q + r0 + c;
-            g[c] = r < n_out ? __ldg(args.dh + obase + (int64_t)r * args.cols) : 0.f;
+          for (int c = 0; c < 16; ++c) {
+            const int r = half_row(i) + c;
+            const int64_t at = obase + (int64_t)r * args.cols;
+            a[c] = r < n_out ? __ldg(args.pre[0] + at) : 0.f;
+            v[c] = r < n_out ? __ldg(args.pre[1] + at) : 0.f;
           }
         };
-        fetch(0);
-        if (!full()) break;
+        if (MODE == Mode::kSwiglu) fetch(0);  // while the unit's products still run
+        ok = __all_sync(0xffffffffu, wait_bounded(ctl.tfull(slot & 1), (slot >> 1) & 1u,
+                                                  ctl.abort_flag, args.err));
+        if (!ok) break;
+        ptx::tc_fence_after();
+        if (MODE == Mode::kSwiglu) {
+          // the accumulator goes back as soon as its last rows have left TMEM
+          const int halves = n_rows > r0 ? 2 * ((n_rows - r0 + 63) / 64) : 0;  // warp-uniform
+          if (halves == 0) ctl.release(slot & 1, lane);
 #pragma unroll 1
-        for (int q = 0; 64 * q < un.n_mma; ++q) {
-          const bool last = 64 * (q + 1) >= un.n_mma;
-          const bool live = 64 * q + r0 < un.n_mma;  // warp-uniform
-          uint32_t h2[16], da2[16], du2[16];
-          if (live) {
-            float a[32], v[32];
-            ptx::tmem_ld32x2(tb + 64 * q, tb + BN + 64 * q, a, v);
+          for (int i = 0; i < halves; ++i) {
+            uint32_t h2[8], da2[8], du2[8];
+            float g[16];
+            ptx::tmem_ld16(tb - r0 + half_row(i), g);
+            if (i == halves - 1) ctl.release(slot & 1, lane);
 #pragma unroll
-            for (int c = 0; c < 16; ++c) {
+            for (int c = 0; c < 8; ++c) {
               float x[2], y[2], z[2];
 #pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                const int k = 2 * c + i;
-                const float sig = sigmoid_f(a[k]);
-                const float silu = a[k] * sig;
-                x[i] = silu * v[k];
-                y[i] = g[k] * v[k] * (sig + silu * (1.0f - sig));
-                z[i] = g[k] * silu;
+              for (int k = 0; k < 2; ++k) {
+                const int n = 2 * c + k;
+                const float sig = sigmoid_f(a[n]);
+                const float silu = a[n] * sig;
+                x[k] = silu * v[n];
+                y[k] = g[n] * v[n] * (sig + silu * (1.0f - sig));
+                z[k] = g[n] * silu;
               }
               const __nv_bfloat162 xb = __floats2bfloat162_rn(x[0], x[1]);
               const __nv_bfloat162 yb = __floats2bfloat162_rn(y[0], y[1]);
@@ -748,71 +783,64 @@ __global__ void __launch_bounds__(kThreads, 1)
               da2[c] = *reinterpret_cast<const uint32_t*>(&yb);
               du2[c] = *reinterpret_cast<const uint32_t*>(&zb);
             }
-          }
-          if (last)
-            ctl.release(acc, lane);
-          else
-            fetch(q + 1);
-          if (!live) continue;
-          uint16_t* h = static_cast<uint16_t*>(args.out) + obase;
-          uint16_t* da = reinterpret_cast<uint16_t*>(args.da) + obase;
-          uint16_t* du = reinterpret_cast<uint16_t*>(args.du) + obase;
+            if (i + 1 < halves) fetch(i + 1);
+            uint16_t* h = static_cast<uint16_t*>(args.out[0]) + obase;
+            uint16_t* da = static_cast<uint16_t*>(args.out[1]) + obase;
+            uint16_t* du = static_cast<uint16_t*>(args.out[2]) + obase;
 #pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            const int r = 64 * q + r0 + c;
-            if (r < n_out) {
-              const int64_t at = (int64_t)r * args.cols;
-              h[at] = (uint16_t)((c & 1) ? h2[c >> 1] >> 16 : h2[c >> 1]);
-              da[at] = (uint16_t)((c & 1) ? da2[c >> 1] >> 16 : da2[c >> 1]);
-              du[at] = (uint16_t)((c & 1) ? du2[c >> 1] >> 16 : du2[c >> 1]);
-            }
-          }
-        }
-      } else {
-        // the whole share leaves TMEM before anything is stored, so the next
-        // unit's products wait for no store
-        constexpr int NQ = BN / 64, kPer = MODE == Mode::kDxF32 ? 32 : 16;
-        uint32_t w[NQ][kPer];
-        if (!full()) break;
-#pragma unroll
-        for (int q = 0; q < NQ; ++q) {
-          if (64 * q + r0 < un.n_mma) {  // warp-uniform
-            float g[32];
-            ptx::tmem_ld32(tb + 64 * q, g);
-#pragma unroll
-            for (int c = 0; c < kPer; ++c) {
-              if (MODE == Mode::kDxF32) {
-                w[q][c] = __float_as_uint(g[c]);
-              } else {
-                const __nv_bfloat162 p = __floats2bfloat162_rn(g[2 * c], g[2 * c + 1]);
-                w[q][c] = *reinterpret_cast<const uint32_t*>(&p);
-              }
-            }
-          }
-        }
-        ctl.release(acc, lane);
-#pragma unroll
-        for (int q = 0; q < NQ; ++q) {
-          if (64 * q + r0 < un.n_mma) {
-#pragma unroll
-            for (int c = 0; c < 32; ++c) {
-              const int r = 64 * q + r0 + c;
+            for (int c = 0; c < 16; ++c) {
+              const int r = half_row(i) + c;
               if (r < n_out) {
-                const int64_t at = obase + (int64_t)r * args.cols;
-                if (MODE == Mode::kDxF32)
-                  static_cast<uint32_t*>(args.out)[at] = w[q][c % kPer];
-                else
-                  static_cast<uint16_t*>(args.out)[at] =
-                      (uint16_t)((c & 1) ? w[q][c / 2 % kPer] >> 16 : w[q][c / 2 % kPer]);
+                const int64_t at = (int64_t)r * args.cols;
+                h[at] = (uint16_t)((c & 1) ? h2[c >> 1] >> 16 : h2[c >> 1]);
+                da[at] = (uint16_t)((c & 1) ? da2[c >> 1] >> 16 : da2[c >> 1]);
+                du[at] = (uint16_t)((c & 1) ? du2[c >> 1] >> 16 : du2[c >> 1]);
+              }
+            }
+          }
+        } else {
+          // the whole share leaves TMEM before anything is stored, so the next
+          // unit's products wait for no store
+          constexpr bool F32 = MODE == Mode::kFwdF32;
+          constexpr int NQ = BN / 64, kPer = F32 ? 32 : 16;
+          uint32_t w[NQ][kPer];
+#pragma unroll
+          for (int q = 0; q < NQ; ++q) {
+            if (64 * q + r0 < n_rows) {  // warp-uniform
+              float g[32];
+              ptx::tmem_ld32(tb + 64 * q, g);
+#pragma unroll
+              for (int c = 0; c < kPer; ++c) {
+                if (F32) {
+                  w[q][c] = __float_as_uint(g[c]);
+                } else {
+                  const __nv_bfloat162 p = __floats2bfloat162_rn(g[2 * c % 32], g[(2 * c + 1) % 32]);
+                  w[q][c] = *reinterpret_cast<const uint32_t*>(&p);
+                }
+              }
+            }
+          }
+          ctl.release(slot & 1, lane);
+#pragma unroll
+          for (int q = 0; q < NQ; ++q) {
+            if (64 * q + r0 < n_rows) {
+#pragma unroll
+              for (int c = 0; c < 32; ++c) {
+                const int r = 64 * q + r0 + c;
+                if (r < n_out) {
+                  const int64_t at = obase + (int64_t)r * args.cols;
+                  if (F32)
+                    static_cast<uint32_t*>(job ? args.out[1] : args.out[0])[at] = w[q][c % kPer];
+                  else
+                    static_cast<uint16_t*>(args.out[0])[at] =
+                        (uint16_t)((c & 1) ? w[q][c / 2 % kPer] >> 16 : w[q][c / 2 % kPer]);
+                }
               }
             }
           }
         }
       }
-      if (++acc == C::kAccBufs) {
-        acc = 0;
-        acc_phase ^= 1u;
-      }
+      next_slot += parts;
     }
   }
   ctl.finish(tmem_base, args.counters);
@@ -1274,7 +1302,7 @@ cudaError_t launch_persistent(void (*kernel)(KArgs...), uint32_t smem,
 
 template <Mode MODE, int BN, bool PAIR>
 cudaError_t run_rows(const RowMaps& maps, const RowArgs& args, cudaStream_t st) {
-  using C = RowCfg<MODE, BN, PAIR>;
+  using C = RowCfg<BN, PAIR>;
   static std::atomic<uint64_t> attr_set{0};
   static std::atomic<int> grids[64];
   return launch_persistent<PAIR>(row_gemm_kernel<MODE, BN, PAIR>, C::kSmemBytes, attr_set, grids,
@@ -1328,23 +1356,26 @@ cudaError_t launch_grouped_rows_tc(const GroupedShape& g, const GroupedJob& job,
   a.k_blocks = (k + BK - 1) / BK;
   a.wide_w = wide;
   a.sources = job.a2 ? 2 : 1;
-  a.out = job.out;
-  if (fwd) return run_rows_sized<Mode::kFwd>(maps, a, st);
-  return job.out_f32 ? run_rows_sized<Mode::kDxF32>(maps, a, st)
-                     : run_rows_sized<Mode::kDx>(maps, a, st);
+  a.out[0] = job.out;
+  return fwd ? run_rows_sized<Mode::kFwd>(maps, a, st) : run_rows_sized<Mode::kDx>(maps, a, st);
 }
 
 cudaError_t launch_swiglu_backward_tc(const GroupedShape& g, const void* x, const void* w_gate,
-                                      const void* w_up, const float* dh, void* h, void* da,
-                                      void* du, int d, int F, const int32_t* offsets,
-                                      int32_t* err, cudaStream_t st) {
-  RowMaps maps;
+                                      const void* w_up, const void* dy, const void* w_down,
+                                      float* pre_a, float* pre_u, void* h, void* da, void* du,
+                                      int d, int F, const int32_t* offsets, int32_t* err,
+                                      cudaStream_t st) {
+  RowMaps up, down;
   const void* w[2] = {w_gate, w_up};
+  const bool wide = F % 64 == 0;
   bool ok = true;
   for (int q = 0; q < 2; ++q) {
-    ok = ok && group_map(&maps.w[q], false, w[q], g.groups, F, d, 64, 128);
+    ok = ok && group_map(&up.w[q], false, w[q], g.groups, F, d, 64, 128) &&
+         (wide ? wide_group_map(&down.w[q], w_down, g.groups, d, F)
+               : group_map(&down.w[q], false, w_down, g.groups, d, F, 64, 64));
     for (int i = 0; i < kRowBoxes; ++i)
-      ok = ok && rows_map(&maps.r[q][i], x, g.rows, d, 128u >> i);
+      ok = ok && rows_map(&up.r[q][i], x, g.rows, d, 128u >> i) &&
+           rows_map(&down.r[q][i], dy, g.rows, d, 128u >> i);
   }
   if (!ok) return cudaErrorInvalidValue;
   RowArgs a = {};
@@ -1356,11 +1387,17 @@ cudaError_t launch_swiglu_backward_tc(const GroupedShape& g, const void* x, cons
   a.cols = F;
   a.k_blocks = (d + BK - 1) / BK;
   a.sources = 1;
-  a.out = h;
-  a.dh = dh;
-  a.da = static_cast<__nv_bfloat16*>(da);
-  a.du = static_cast<__nv_bfloat16*>(du);
-  return run_rows_sized<Mode::kGateUp>(maps, a, st);
+  a.out[0] = pre_a;
+  a.out[1] = pre_u;
+  const cudaError_t e = run_rows_sized<Mode::kFwdF32>(up, a, st);
+  if (e != cudaSuccess) return e;
+  a.wide_w = wide;
+  a.pre[0] = pre_a;
+  a.pre[1] = pre_u;
+  a.out[0] = h;
+  a.out[1] = da;
+  a.out[2] = du;
+  return run_rows_sized<Mode::kSwiglu>(down, a, st);
 }
 
 cudaError_t launch_grouped_dw_tc(const GroupedShape& g, const GroupedJob* jobs, int n_jobs,

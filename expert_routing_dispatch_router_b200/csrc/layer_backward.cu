@@ -241,7 +241,7 @@ __global__ void __launch_bounds__(kDwThreads)
   __shared__ float s_dl[kDwChunk];
   griddep_wait();
   griddep_launch_dependents();
-  segment_table<kDwThreads>(offsets, E, slots, kDwChunk, s_off, s_tile, s_warp);
+  segment_table<kDwThreads>(offsets, E, slots, kDwChunk, 0, s_off, s_tile, s_warp);
   if (blockIdx.x == 0)
     for (int i = threadIdx.x; i <= E; i += kDwThreads) chunk_start[i] = s_tile[i];
   const int cb = (int)((d + kDwThreads * V - 1) / (kDwThreads * V));
@@ -472,10 +472,12 @@ BackwardWs backward_ws(const Shape& sh) {
   const size_t Tk = (size_t)(sh.T * sh.k), act = (size_t)sh.es;
   const bool routed = sh.N > 0;
   L.header = take(256);
-  L.dh = take(routed ? Tk * sh.F * 4 : 0);
+  L.pre_a = take(routed ? Tk * sh.F * 4 : 0);
+  L.pre_u = take(routed ? Tk * sh.F * 4 : 0);
+  L.dh = take(routed && !sh.bf16 ? Tk * sh.F * 4 : 0);
   L.h = take(routed ? Tk * sh.F * act : 0);
-  L.da = take(routed ? Tk * sh.F * act : 0);
-  L.du = take(routed ? Tk * sh.F * act : 0);
+  L.da = take(routed && sh.bf16 ? Tk * sh.F * 2 : 0);
+  L.du = take(routed && sh.bf16 ? Tk * sh.F * 2 : 0);
   L.dy_perm = take(routed ? Tk * sh.d * act : 0);
   L.dx_perm = take(routed ? Tk * sh.d * act : 0);
   L.dgate = take(Tk * 4);
@@ -522,18 +524,24 @@ cudaError_t launch_expert_ffn_backward(const Shape& sh, const void* x_perm,
   const BackwardWs L = backward_ws(sh);
   const GroupedShape g{sh.T * sh.k, (int)sh.N, sh.bf16};
   int32_t* err = at<int32_t>(ws, L.header);
-  float* dh = at<float>(ws, L.dh);
-  void *h = at<void>(ws, L.h), *da = at<void>(ws, L.da), *du = at<void>(ws, L.du);
+  float *pre_a = at<float>(ws, L.pre_a), *pre_u = at<float>(ws, L.pre_u);
+  void* h = at<void>(ws, L.h);
+  void* da = sh.bf16 ? at<void>(ws, L.da) : pre_a;
+  void* du = sh.bf16 ? at<void>(ws, L.du) : pre_u;
   const int d = (int)sh.d, F = (int)sh.F;
-  const GroupedJob pre[3] = {
-      {Form::kDx, dy_perm, w_down, nullptr, nullptr, dh, F, d, true},
-      {Form::kFwd, x_perm, w_gate, nullptr, nullptr, da, d, F, true},
-      {Form::kFwd, x_perm, w_up, nullptr, nullptr, du, d, F, true}};
-  cudaError_t e = launch_grouped_jobs(g, pre, sh.bf16 ? 1 : 3, offsets, err, st);
-  if (e != cudaSuccess) return e;
-  e = sh.bf16 ? launch_swiglu_backward_tc(g, x_perm, w_gate, w_up, dh, h, da, du, d, F, offsets,
-                                          err, st)
-              : swiglu_backward(sh, dh, offsets, h, da, du, st);
+  cudaError_t e;
+  if (sh.bf16) {
+    e = launch_swiglu_backward_tc(g, x_perm, w_gate, w_up, dy_perm, w_down, pre_a, pre_u, h, da,
+                                  du, d, F, offsets, err, st);
+  } else {
+    float* dh = at<float>(ws, L.dh);
+    const GroupedJob pre[3] = {{Form::kDx, dy_perm, w_down, nullptr, nullptr, dh, F, d, true},
+                               {Form::kFwd, x_perm, w_gate, nullptr, nullptr, pre_a, d, F, true},
+                               {Form::kFwd, x_perm, w_up, nullptr, nullptr, pre_u, d, F, true}};
+    e = launch_grouped_jobs(g, pre, 3, offsets, err, st);
+    if (e != cudaSuccess) return e;
+    e = swiglu_backward(sh, dh, offsets, h, da, du, st);
+  }
   if (e != cudaSuccess) return e;
   const GroupedJob dx{Form::kDx, da, w_gate, du, w_up, dx_perm, d, F, false};
   e = launch_grouped_jobs(g, &dx, 1, offsets, err, st);
