@@ -339,8 +339,9 @@ struct Control {
   volatile int* abort_flag;
   uint32_t* tmem_slot;
   volatile int* ring;
-  __device__ uint32_t ring_full(int r) const { return bars + 224u + 8u * r; }
-  __device__ uint32_t ring_empty(int r) const { return bars + 256u + 8u * r; }
+  static constexpr uint32_t kRingOff = 8 * (2 * S + 6);  // behind the barriers and tmem_slot
+  __device__ uint32_t ring_full(int r) const { return bars + kRingOff + 8u * r; }
+  __device__ uint32_t ring_empty(int r) const { return bars + kRingOff + 32u + 8u * r; }
   // counters: [0] next unit, [1] CTAs (pairs) that have finished
   __device__ bool publish(int seq, int u, int32_t* err) const {
     const int r = seq % kRing;
@@ -401,11 +402,11 @@ struct Control {
   __device__ uint32_t tempty(int b) const { return bars + 8u * (2 * S + 2 + b); }
   __device__ uint32_t mma_done() const { return bars + 8u * (2 * S + 4); }
   __device__ void init(uint8_t* smem, uint32_t sbase, uint32_t bar_off) {
-    static_assert(8 * (2 * S + 5) + 8 <= 224, "barriers fit their bytes");
+    static_assert(kRing == 4 && kRingOff + 80 <= kCtlBytes, "barriers fit their bytes");
     bars = sbase + bar_off;
     tmem_slot = reinterpret_cast<uint32_t*>(smem + bar_off + 8 * (2 * S + 5));
     abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    ring = reinterpret_cast<volatile int*>(smem + bar_off + 288);
+    ring = reinterpret_cast<volatile int*>(smem + bar_off + kRingOff + 64);
     if (threadIdx.x == 0) {
       for (int s = 0; s < S; ++s) {
         ptx::mbar_init(full(s), 1);
@@ -876,14 +877,14 @@ struct DwArgs {
 // operands come from L2 at about 64 bytes a clock and SM).
 struct DwCfg {
   static constexpr int kRun = 8;
-  static constexpr int kASlots = 6, kBSlots = 5;
+  static constexpr int kASlots = 5, kBSlots = 7;
   static constexpr uint32_t kSlotBytes = 2 * kBlockBytes;  // 128 columns x 64 rows
   static constexpr uint32_t kOutBuf = 4096;  // one warp's 32 rows x 128 bytes
   static constexpr uint32_t kBOff = kASlots * kSlotBytes;
   static constexpr uint32_t kOutOff = kBOff + kBSlots * kSlotBytes;
   static constexpr uint32_t kBarOff = kOutOff + kEpiWarps * kOutBuf;
-  static constexpr uint32_t kOffOff = kBarOff + kCtlBytes;
-  static constexpr uint32_t kSmemBytes = 1024 + kOffOff + 4 * (kMaxExperts + 1);
+  static constexpr uint32_t kSmemBytes = 1024 + kBarOff + kCtlBytes;
+  static_assert(kSmemBytes <= 232448, "shared memory of a CTA");
 };
 
 struct DwUnit {
@@ -896,8 +897,10 @@ __host__ __device__ __forceinline__ int dw_runs(int n_in) {
   return (nj + DwCfg::kRun - 1) / DwCfg::kRun;
 }
 
+// The offsets are read where a unit is taken up (clamped as segment_table
+// does); shared memory is all operand slots.
 __device__ __forceinline__ DwUnit dw_unit(int u, const int* first, const DwMaps& maps,
-                                          const int32_t* s_off) {
+                                          const DwArgs& args) {
   DwUnit un;
   un.job = u >= first[2] ? 2 : (u >= first[1] ? 1 : 0);
   const DwJob& j = maps.job[un.job];
@@ -908,9 +911,11 @@ __device__ __forceinline__ DwUnit dw_unit(int u, const int* first, const DwMaps&
   un.e = v / runs / ni;
   un.jt0 = nj * run / runs;
   un.jt1 = nj * (run + 1) / runs;
-  un.row0 = s_off[un.e];
-  const int n = s_off[un.e + 1] - un.row0;
-  un.n_rows = n > 0 ? n : 0;
+  const int rows = (int)args.rows;
+  const int lo = __ldg(args.offsets + un.e), hi = __ldg(args.offsets + un.e + 1);
+  un.row0 = lo < 0 ? 0 : (lo > rows ? rows : lo);
+  const int end = hi < 0 ? 0 : (hi > rows ? rows : hi);
+  un.n_rows = end > un.row0 ? end - un.row0 : 0;
   return un;
 }
 
@@ -967,7 +972,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const uint32_t sbase = ptx::smem_addr(smem);
-  int32_t* s_off = reinterpret_cast<int32_t*>(smem + C::kOffOff);
   // slots 0..SA-1 hold dy, SA..SA+SB-1 hold x; one pair of barriers each
   Control<SA + SB, true> ctl;
   ctl.init(smem, sbase, C::kBarOff);
@@ -975,10 +979,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t rank = G::rank();
   griddep_wait();
   griddep_launch_dependents();
-  for (int i = threadIdx.x; i <= args.groups; i += kThreads) {
-    const int32_t o = args.offsets[i];
-    s_off[i] = o < 0 ? 0 : (o > args.rows ? (int32_t)args.rows : o);
-  }
   ptx::tc_fence_before();
   __syncthreads();
   G::sync_all();
@@ -1020,7 +1020,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int seq = 0, u; ok; ++seq) {
       ok = ctl.next(seq, total, args.counters, &claimed, &u, args.err);
       if (!ok || u < 0) break;
-      const DwUnit un = dw_unit(u, first_unit, maps, s_off);
+      const DwUnit un = dw_unit(u, first_unit, maps, args);
       const DwJob& job = maps.job[un.job];
       const bool wide_a = job.n_out % 64 == 0, wide_b = job.n_in % 64 == 0;
       const int acol = (un.it * 2 + (int)rank) * BM;
@@ -1059,7 +1059,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int seq = 0, u; ok; ++seq) {
         ok = ctl.take_warp(seq, &u, args.err);
         if (!ok || u < 0) break;
-        const DwUnit un = dw_unit(u, first_unit, maps, s_off);
+        const DwUnit un = dw_unit(u, first_unit, maps, args);
         if (un.n_rows == 0) continue;  // the epilogue writes zeros by itself
         const bool keep = un.n_rows <= SA * BK;
         const int sa0 = sa;
@@ -1129,7 +1129,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t acc_phase = 0;
     bool ok = true;
     for (int seq = 0, u; ok && ctl.take_warp(seq, &u, args.err) && u >= 0; ++seq) {
-      const DwUnit un = dw_unit(u, first_unit, maps, s_off);
+      const DwUnit un = dw_unit(u, first_unit, maps, args);
       const DwJob& job = maps.job[un.job];
       const int n_out = job.n_out, n_in = job.n_in;
       const int row = (un.it * 2 + (int)rank) * BM + ew * 32;
