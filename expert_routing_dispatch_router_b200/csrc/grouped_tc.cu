@@ -43,6 +43,7 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 320;
+constexpr int kDwThreads = 352;  // weight gradients: warp 10 loads the second operand
 constexpr int kEpiWarps = 8;
 constexpr int BM = 128;  // output columns (row products) or rows (dw) per CTA
 constexpr int BK = 64;   // contraction elements per stage
@@ -330,10 +331,10 @@ constexpr uint32_t kCtlBytes = 320;
 // The (leader's) producer publishes each unit id, -1 at the end, in a ring of
 // kRing slots in its own and its peer's shared memory; the other roles read
 // their units from there. A slot is free again when its readers have arrived on
-// the publisher's ring_empty: the MMA thread, the epilogue warps and, in a
-// pair, the peer's producer and epilogue warps. The last CTA (pair) to finish
-// returns the counters to zero.
-template <int S, bool PAIR>
+// the publisher's ring_empty: the MMA warp, the epilogue warps, a second
+// producer if there is one (TWO) and, in a pair, the peer's producers and
+// epilogue warps. The last CTA (pair) to finish returns the counters to zero.
+template <int S, bool PAIR, bool TWO>
 struct Control {
   uint32_t bars;
   volatile int* abort_flag;
@@ -419,7 +420,7 @@ struct Control {
       ptx::mbar_init(mma_done(), 1);
       for (int r = 0; r < kRing; ++r) {
         ptx::mbar_init(ring_full(r), 1);
-        ptx::mbar_init(ring_empty(r), 1 + kEpiWarps + (PAIR ? 1 + kEpiWarps : 0));
+        ptx::mbar_init(ring_empty(r), (1 + kEpiWarps + TWO) * (PAIR ? 2 : 1));
       }
       *abort_flag = 0;
       ptx::fence_mbar_init();
@@ -560,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   int32_t* s_tile = reinterpret_cast<int32_t*>(smem + C::kTabOff);
   int32_t* s_off = s_tile + (kMaxExperts + 1);
   int32_t* s_warp = s_off + (kMaxExperts + 1);
-  Control<S, PAIR> ctl;
+  Control<S, PAIR, false> ctl;
   ctl.init(smem, sbase, C::kBarOff);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = G::rank();
@@ -963,7 +964,7 @@ __device__ __forceinline__ void dw_load(const CUtensorMap* maps, bool wide, uint
 }
 
 template <bool OUT_F32>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kDwThreads, 1)
     dw_gemm_kernel(const __grid_constant__ DwMaps maps, const DwArgs args) {
   using C = DwCfg;
   using G = Cg<true>;
@@ -973,7 +974,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const uint32_t sbase = ptx::smem_addr(smem);
   // slots 0..SA-1 hold dy, SA..SA+SB-1 hold x; one pair of barriers each
-  Control<SA + SB, true> ctl;
+  Control<SA + SB, true, true> ctl;
   ctl.init(smem, sbase, C::kBarOff);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = G::rank();
@@ -995,52 +996,48 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   const int total = first_unit[kMaxJobs];
 
-  if (warp == 0) {
-    // ---------------------------------------------------- TMA producer --
+  if (warp == 0 || warp == 10) {
+    // --------------------------------------------------- TMA producers --
+    // Warp 0 loads dy and hands out the units, warp 10 loads x: a slot costs its
+    // producer about 380 cycles (wait, arm, copy, loop), and one warp for both
+    // took longer than the products of a 64-row block, 512.
+    const bool load_b = warp == 10;
     const bool elected = elect_one();
     const uint64_t pol = ptx::policy_evict_normal();
     const uint32_t full0 = G::at_leader(ctl.full(0));
     const int oob = (int)args.rows;
-    int sa = 0, sb = 0, claimed = 0;
-    uint32_t pa = 0, pb = 0, armed = 0, armed_par = 0;
+    const int base = load_b ? SA : 0, slots = load_b ? SB : SA;
+    int slot = 0, claimed = 0;
+    uint32_t phase = 0, armed = 0, armed_par = 0;
     bool ok = true;
-    // waits for a slot and fills it with 128 columns of rows r0 .. r0 + n - 1
-    auto fill = [&](int slot, uint32_t par, const CUtensorMap* m, bool wide, int x, int r0,
-                    int n) -> bool {
-      if (!wait_warp(ctl.empty(slot), par ^ 1u, ctl.abort_flag, args.err)) return false;
-      if (elected) {
-        if (rank == 0)
-          ptx::mbar_arrive_expect_tx(ctl.full(slot), 2u * 2u * 128u * (uint32_t)((n + 15) & ~15));
-        dw_load(m, wide, sbase + slot * C::kSlotBytes, full0 + 8u * slot, x, r0, n, oob, pol);
-      }
-      armed |= 1u << slot;
-      armed_par = (armed_par & ~(1u << slot)) | (par << slot);
-      return true;
-    };
     for (int seq = 0, u; ok; ++seq) {
-      ok = ctl.next(seq, total, args.counters, &claimed, &u, args.err);
+      ok = load_b ? ctl.take_warp(seq, &u, args.err)
+                  : ctl.next(seq, total, args.counters, &claimed, &u, args.err);
       if (!ok || u < 0) break;
       const DwUnit un = dw_unit(u, first_unit, maps, args);
       const DwJob& job = maps.job[un.job];
-      const bool wide_a = job.n_out % 64 == 0, wide_b = job.n_in % 64 == 0;
-      const int acol = (un.it * 2 + (int)rank) * BM;
-      const bool keep = un.n_rows <= SA * BK;
-      for (int jt = un.jt0; jt < un.jt1 && ok; ++jt) {
-        const int bcol = jt * 256 + (int)rank * 128;
+      const CUtensorMap* m = load_b ? job.b : job.a;
+      const bool wide = (load_b ? job.n_in : job.n_out) % 64 == 0;
+      // a dy panel that is kept is loaded once, for the first tile of the run
+      const int jt1 = load_b || un.n_rows > SA * BK ? un.jt1 : un.jt0 + 1;
+      for (int jt = un.jt0; jt < jt1 && ok; ++jt) {
+        const int x = load_b ? jt * 256 + (int)rank * 128 : (un.it * 2 + (int)rank) * BM;
         for (int k0 = 0; k0 < un.n_rows; k0 += BK) {
-          const int left = un.n_rows - k0;
-          const int n = left < BK ? left : BK;
-          if (jt == un.jt0 || !keep) {
-            if (!(ok = fill(sa, pa, job.a, wide_a, acol, un.row0 + k0, n))) break;
-            if (++sa == SA) {
-              sa = 0;
-              pa ^= 1u;
-            }
+          const int n = un.n_rows - k0 < BK ? un.n_rows - k0 : BK;
+          const int at = base + slot;
+          if (!(ok = wait_warp(ctl.empty(at), phase ^ 1u, ctl.abort_flag, args.err))) break;
+          if (elected) {
+            if (rank == 0)
+              ptx::mbar_arrive_expect_tx(ctl.full(at),
+                                         2u * 2u * 128u * (uint32_t)((n + 15) & ~15));
+            dw_load(m, wide, sbase + at * C::kSlotBytes, full0 + 8u * at, x, un.row0 + k0, n, oob,
+                    pol);
           }
-          if (!(ok = fill(SA + sb, pb, job.b, wide_b, bcol, un.row0 + k0, n))) break;
-          if (++sb == SB) {
-            sb = 0;
-            pb ^= 1u;
+          armed |= 1u << at;
+          armed_par = (armed_par & ~(1u << at)) | (phase << at);
+          if (++slot == slots) {
+            slot = 0;
+            phase ^= 1u;
           }
         }
       }
@@ -1260,7 +1257,7 @@ bool wide_group_map(CUtensorMap* map, const void* base, int groups, int n_out, i
 
 // Persistent launch: one CTA per SM, or as many pairs as can be resident.
 template <bool PAIR, typename... KArgs, typename... Args>
-cudaError_t launch_persistent(void (*kernel)(KArgs...), uint32_t smem,
+cudaError_t launch_persistent(void (*kernel)(KArgs...), int threads, uint32_t smem,
                               std::atomic<uint64_t>& attr_set, std::atomic<int>* grids,
                               cudaStream_t st, Args&&... args) {
   int dev = 0;
@@ -1269,7 +1266,7 @@ cudaError_t launch_persistent(void (*kernel)(KArgs...), uint32_t smem,
   e = raise_smem_once(attr_set, kernel, (int)smem);
   if (e != cudaSuccess) return e;
   if (!PAIR)
-    return launch_pdl(kernel, dim3(num_sms()), dim3(kThreads), smem, st,
+    return launch_pdl(kernel, dim3(num_sms()), dim3(threads), smem, st,
                       std::forward<Args>(args)...);
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -1279,7 +1276,7 @@ cudaError_t launch_persistent(void (*kernel)(KArgs...), uint32_t smem,
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cfg.attrs = attr;
@@ -1305,8 +1302,8 @@ cudaError_t run_rows(const RowMaps& maps, const RowArgs& args, cudaStream_t st) 
   using C = RowCfg<BN, PAIR>;
   static std::atomic<uint64_t> attr_set{0};
   static std::atomic<int> grids[64];
-  return launch_persistent<PAIR>(row_gemm_kernel<MODE, BN, PAIR>, C::kSmemBytes, attr_set, grids,
-                                 st, maps, args);
+  return launch_persistent<PAIR>(row_gemm_kernel<MODE, BN, PAIR>, kThreads, C::kSmemBytes,
+                                 attr_set, grids, st, maps, args);
 }
 
 template <Mode MODE>
@@ -1323,7 +1320,7 @@ template <bool OUT_F32>
 cudaError_t run_dw(const DwMaps& maps, const DwArgs& args, cudaStream_t st) {
   static std::atomic<uint64_t> attr_set{0};
   static std::atomic<int> grids[64];
-  return launch_persistent<true>(dw_gemm_kernel<OUT_F32>, DwCfg::kSmemBytes,
+  return launch_persistent<true>(dw_gemm_kernel<OUT_F32>, kDwThreads, DwCfg::kSmemBytes,
                                  attr_set, grids, st, maps, args);
 }
 
