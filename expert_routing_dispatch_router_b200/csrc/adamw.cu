@@ -40,7 +40,7 @@ constexpr int kAdamTable = 1024;  // tensors whose first blocks fit in shared me
 struct AdamState {  // moe_adamw_step's `state`, on the device
   int64_t step;
   float size;  // lr / (1 - b1^t)
-  float root;  // sqrt(1 - b2^t)
+  float inv_root;  // 1 / sqrt(1 - b2^t)
 };
 
 struct AdamArgs {
@@ -61,7 +61,7 @@ __global__ void adamw_coef_kernel(AdamState* st, double lr, double b1, double b2
   const int64_t t = st->step + 1;
   st->step = t;
   st->size = (float)(lr / (1.0 - pow(b1, (double)t)));
-  st->root = (float)sqrt(1.0 - pow(b2, (double)t));
+  st->inv_root = (float)(1.0 / sqrt(1.0 - pow(b2, (double)t)));
 }
 
 template <typename T>
@@ -123,36 +123,58 @@ __device__ __forceinline__ void save8<__nv_bfloat16>(__nv_bfloat16* p, int n, co
   }
 }
 
-// Eight e4m3 codes times their block's scale.
+// Eight e4m3 codes times their block's scale (every e4m3 value is exact in
+// half precision, which the conversion goes through).
 __device__ __forceinline__ void widen8(const uint8_t* p, float scale, float* v) {
   const uint2 u = *reinterpret_cast<const uint2*>(p);
   const uint32_t w[2] = {u.x, u.y};
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    __nv_fp8_e4m3 c;
-    c.__x = (__nv_fp8_storage_t)((w[i >> 2] >> (8 * (i & 3))) & 0xffu);
-    v[i] = __fmul_rn((float)c, scale);
+  for (int i = 0; i < 4; ++i) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
+        (__nv_fp8x2_storage_t)((w[i >> 1] >> (16 * (i & 1))) & 0xffffu), __NV_E4M3);
+    const float2 f = __half22float2(__half2(h));
+    v[2 * i] = __fmul_rn(f.x, scale);
+    v[2 * i + 1] = __fmul_rn(f.y, scale);
   }
 }
 
 // Codes of 8 values of a block and the block's scale. The maximum is taken on
 // the magnitudes' bits, so a NaN (larger than infinity there) reaches the
-// scale instead of being passed over.
+// scale instead of being passed over. The quotients by the block's one scale
+// are correctly rounded by Markstein's method (IBM J. Res. Dev. 34, 1990): from
+// y = 1 / scale rounded, q = v y, and q + (v - q scale) y with fused
+// operations. Scales whose reciprocal or remainders would leave the normal
+// range (and NaN) take the divide.
 template <bool ROOT>
 __device__ __forceinline__ void narrow8(const float* v, uint8_t* p, float* scale_out, int lane) {
   uint32_t top = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
+  top = __reduce_max_sync(0xffffffffu, top);
   const float scale = __fmul_rn(__uint_as_float(top), 1.0f / 448.0f);
   uint32_t w[2] = {0, 0};
   if (scale > 0.f) {
+    float q[8];
+    if (scale > 1e-18f && scale < 1e18f) {
+      const float y = __frcp_rn(scale);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float q = __fdiv_rn(v[i], scale);
-      if (ROOT && q > 0.f && q < 0.001953125f) q = 0.001953125f;  // 2^-9, the smallest step
-      w[i >> 2] |= (uint32_t)__nv_cvt_float_to_fp8(q, __NV_SATFINITE, __NV_E4M3) << (8 * (i & 3));
+      for (int i = 0; i < 8; ++i) {
+        const float q0 = __fmul_rn(v[i], y);
+        q[i] = __fmaf_rn(__fmaf_rn(-q0, scale, v[i]), y, q0);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) q[i] = __fdiv_rn(v[i], scale);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float2 f = make_float2(q[2 * i], q[2 * i + 1]);
+      if (ROOT) {  // 2^-9 is the smallest step
+        if (f.x > 0.f) f.x = fmaxf(f.x, 0.001953125f);
+        if (f.y > 0.f) f.y = fmaxf(f.y, 0.001953125f);
+      }
+      w[i >> 1] |= (uint32_t)__nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3)
+                   << (16 * (i & 1));
     }
   }
   *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
@@ -169,7 +191,7 @@ __global__ void __launch_bounds__(kAdamThreads) adamw_kernel(const AdamArgs a) {
   if (in_smem)
     for (int i = threadIdx.x; i < n_t; i += kAdamThreads) s_first[i] = a.table[i].first_block;
   __syncthreads();
-  const float size = a.state->size, root = a.state->root;
+  const float size = a.state->size, inv_root = a.state->inv_root;
   const int lane = threadIdx.x & 31;
   const int64_t warps = (int64_t)gridDim.x * (kAdamThreads / 32);
   for (int64_t b = (int64_t)blockIdx.x * (kAdamThreads / 32) + (threadIdx.x >> 5); b < a.blocks;
@@ -207,7 +229,8 @@ __global__ void __launch_bounds__(kAdamThreads) adamw_kernel(const AdamArgs a) {
       m[i] = __fadd_rn(__fmul_rn(m[i], a.b1), __fmul_rn(g[i], a.omb1));
       v[i] = __fadd_rn(__fmul_rn(v[i], a.b2), __fmul_rn(__fmul_rn(g[i], a.omb2), g[i]));
       r[i] = __fsqrt_rn(v[i]);
-      const float step = __fdiv_rn(m[i], __fadd_rn(__fdiv_rn(r[i], root), a.eps));
+      // the weights' quotient takes the fast divide (2 units), like its root
+      const float step = __fdividef(m[i], __fmaf_rn(r[i], inv_root, a.eps));
       p[i] = __fsub_rn(__fmul_rn(p[i], a.keep), __fmul_rn(step, size));
     }
     if (tn.master) save8<float>(tn.master + at, n, p);

@@ -25,6 +25,7 @@ struct Chunk<__nv_bfloat16> {
   static constexpr int n = 8;
   uint4 u;
   __device__ void load(const __nv_bfloat16* p) { u = __ldg(reinterpret_cast<const uint4*>(p)); }
+  __device__ void load_any(const __nv_bfloat16* p) { u = *reinterpret_cast<const uint4*>(p); }
   __device__ void zero() { u = make_uint4(0, 0, 0, 0); }
   __device__ float get(int i) const {
     const uint32_t w = i < 2 ? u.x : (i < 4 ? u.y : (i < 6 ? u.z : u.w));
@@ -45,6 +46,7 @@ struct Chunk<float> {
   static constexpr int n = 4;
   float4 f;
   __device__ void load(const float* p) { f = __ldg(reinterpret_cast<const float4*>(p)); }
+  __device__ void load_any(const float* p) { f = *reinterpret_cast<const float4*>(p); }
   __device__ void zero() { f = make_float4(0.f, 0.f, 0.f, 0.f); }
   __device__ float get(int i) const {
     return i == 0 ? f.x : (i == 1 ? f.y : (i == 2 ? f.z : f.w));
@@ -61,13 +63,17 @@ __device__ __forceinline__ float sum_warp(float v) {
 }
 
 // ------------------------------------------------------- combine backward --
-constexpr int kCbThreads = 256;
-constexpr int kSlotGroup = 8;  // rows of y in flight together
+constexpr int kSlotGroup = 8;  // 16-byte loads in flight together
+constexpr int kCbThreads = 128;
+constexpr size_t kCbStage = 40 * 1024;  // dout rows up to this size are staged
 
-// One block per token: the token's dout passes through registers once, and
-// meets every slot's expert output there. KMAX >= k sums live in registers.
-// A slot whose id or row is outside the buffers gets a zero gate gradient.
-template <typename AT, int KMAX>
+// One block per token, one warp per slot at a time: the warp reads the slot's
+// expert output once, multiplies it into dout and writes dout times the gate.
+// The token's dout row is staged in shared memory (STAGE; longer rows are read
+// again from L2). Bound by HBM: y in, dy out. A slot whose id or row is outside
+// the buffers gets a zero gate gradient; all zero-expert slots of a token share
+// one sum.
+template <typename AT, bool STAGE>
 __global__ void __launch_bounds__(kCbThreads)
     combine_backward_kernel(const AT* __restrict__ dout, const AT* __restrict__ x,
                             const AT* __restrict__ y, const int32_t* __restrict__ idx,
@@ -75,88 +81,89 @@ __global__ void __launch_bounds__(kCbThreads)
                             const int32_t* __restrict__ slot_row, AT* __restrict__ dy,
                             float* __restrict__ dgate, int64_t d, int N, int E, int k, float s,
                             int64_t rows) {
-  constexpr int V = Chunk<AT>::n;
+  constexpr int V = Chunk<AT>::n, W = kCbThreads / 32;
+  extern __shared__ __align__(16) uint8_t s_raw[];
+  AT* s_dout = reinterpret_cast<AT*>(s_raw);
   __shared__ int32_t s_row[kMaxTopK];  // row, -1: zero expert, -2: nothing
   __shared__ float s_gate[kMaxTopK];
-  __shared__ float s_sum[kCbThreads / 32][kMaxTopK + 1];
+  __shared__ float s_zero;
   griddep_wait();
   griddep_launch_dependents();
   const int64_t t = blockIdx.x;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if ((int)threadIdx.x < k) {
     const int e = idx[t * k + threadIdx.x];
     const int r = slot_row[t * k + threadIdx.x];
     s_row[threadIdx.x] = e < 0 || e >= E ? -2 : (e >= N ? -1 : (r < 0 || r >= rows ? -2 : r));
     s_gate[threadIdx.x] = s * gate[t * k + threadIdx.x];
   }
+  if (STAGE) {
+    const uint4* src = reinterpret_cast<const uint4*>(dout + t * d);
+    uint4* dst = reinterpret_cast<uint4*>(s_dout);
+    for (int i = threadIdx.x; i < (int)(d / V); i += kCbThreads) dst[i] = __ldg(src + i);
+  }
   __syncthreads();
-  bool any_zero = false;
-  for (int j = 0; j < k; ++j) any_zero |= s_row[j] == -1;
-  float acc[KMAX], acc_x = 0.f;
-#pragma unroll
-  for (int j = 0; j < KMAX; ++j) acc[j] = 0.f;
-  for (int64_t c = (int64_t)threadIdx.x * V; c < d; c += (int64_t)kCbThreads * V) {
-    Chunk<AT> g, xv;
-    g.load(dout + t * d + c);
-    if (any_zero)
-      xv.load(x + t * d + c);
-    else
-      xv.zero();
-#pragma unroll
-    for (int j0 = 0; j0 < KMAX; j0 += kSlotGroup) {
-      Chunk<AT> yv[kSlotGroup];
+  const AT* row = STAGE ? s_dout : dout + t * d;
+  int first_zero = -1;
+  for (int j = 0; j < k; ++j)
+    if (first_zero < 0 && s_row[j] == -1) first_zero = j;
+  // warp w takes the routed slots and, once, the zero experts' sum, in turn
+  int turn = 0;
+  for (int j = 0; j < k; ++j) {
+    const int r = s_row[j];
+    if (r < 0 && j != first_zero) continue;
+    if (turn++ % W != warp) continue;
+    const bool routed = r >= 0;
+    const AT* in = routed ? y + (int64_t)r * d : x + t * d;
+    AT* out = dy + (int64_t)(routed ? r : 0) * d;
+    const float g = s_gate[j];
+    float acc = 0.f;
+    for (int64_t c0 = (int64_t)lane * V; c0 < d; c0 += 32 * V * kSlotGroup) {
+      Chunk<AT> v[kSlotGroup];
 #pragma unroll
       for (int q = 0; q < kSlotGroup; ++q) {
-        const int j = j0 + q;
-        if (j < k && s_row[j] >= 0)
-          yv[q].load(y + (int64_t)s_row[j] * d + c);
+        const int64_t c = c0 + q * 32 * V;
+        if (c < d)
+          v[q].load(in + c);
         else
-          yv[q].zero();
+          v[q].zero();
       }
 #pragma unroll
       for (int q = 0; q < kSlotGroup; ++q) {
-        const int j = j0 + q;
-        if (j < k && s_row[j] >= 0) {
-          float v[V];
+        const int64_t c = c0 + q * 32 * V;
+        if (c >= d) continue;
+        Chunk<AT> b;
+        b.load_any(row + c);
+        float o[V];
 #pragma unroll
-          for (int i = 0; i < V; ++i) {
-            acc[j] = fmaf(g.get(i), yv[q].get(i), acc[j]);
-            v[i] = s_gate[j] * g.get(i);
-          }
-          Chunk<AT>::store(dy + (int64_t)s_row[j] * d + c, v);
+        for (int i = 0; i < V; ++i) {
+          acc = fmaf(b.get(i), v[q].get(i), acc);
+          o[i] = g * b.get(i);
         }
+        if (routed) Chunk<AT>::store(out + c, o);
       }
     }
-    if (any_zero) {
-#pragma unroll
-      for (int i = 0; i < V; ++i) acc_x = fmaf(g.get(i), xv.get(i), acc_x);
+    acc = sum_warp(acc);
+    if (lane == 0) {
+      if (routed)
+        dgate[t * k + j] = s * acc;
+      else
+        s_zero = acc;
     }
   }
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-#pragma unroll
-  for (int j = 0; j < KMAX; ++j) {
-    const float v = sum_warp(acc[j]);
-    if (lane == 0 && j < k) s_sum[warp][j] = v;
-  }
-  acc_x = sum_warp(acc_x);
-  if (lane == 0) s_sum[warp][kMaxTopK] = acc_x;
   __syncthreads();
-  if ((int)threadIdx.x < k) {
-    const int r = s_row[threadIdx.x];
-    float v = 0.f;
-    for (int w = 0; w < kCbThreads / 32; ++w)
-      v += s_sum[w][r == -1 ? kMaxTopK : threadIdx.x];
-    dgate[t * k + threadIdx.x] = r == -2 ? 0.f : (r == -1 ? v : s * v);
-  }
+  if ((int)threadIdx.x < k && s_row[threadIdx.x] < 0)
+    dgate[t * k + threadIdx.x] = s_row[threadIdx.x] == -1 ? s_zero : 0.f;
 }
 
 template <typename AT>
 cudaError_t combine_backward(const Shape& sh, const void* dout, const void* x, const void* y,
                              const int32_t* idx, const float* gate, const int32_t* slot_row,
                              void* dy, float* dgate, cudaStream_t st) {
-  auto kernel = sh.k <= 8    ? combine_backward_kernel<AT, 8>
-                : sh.k <= 16 ? combine_backward_kernel<AT, 16>
-                             : combine_backward_kernel<AT, 32>;
-  return launch_pdl(kernel, dim3((unsigned)sh.T), dim3(kCbThreads), 0, st,
+  const size_t bytes = (size_t)sh.d * sizeof(AT);
+  const bool stage = bytes <= kCbStage;
+  return launch_pdl(stage ? combine_backward_kernel<AT, true> : combine_backward_kernel<AT, false>,
+                    dim3((unsigned)sh.T), dim3(kCbThreads), stage ? bytes : 0, st,
                     static_cast<const AT*>(dout), static_cast<const AT*>(x),
                     static_cast<const AT*>(y), idx, gate, slot_row, static_cast<AT*>(dy), dgate,
                     sh.d, (int)sh.N, (int)sh.E, (int)sh.k, sh.s, sh.T * sh.k);
