@@ -85,8 +85,12 @@ class GroupedShape:
     dtype: torch.dtype = torch.bfloat16
 
     def c(self) -> MoEGrouped:
-        return MoEGrouped(self.rows, self.groups, self.n_in, self.n_out,
-                          _DTYPE_CODE[self.dtype])
+        c = self.__dict__.get("_c")  # built once: a frozen shape does not change
+        if c is None:
+            c = MoEGrouped(self.rows, self.groups, self.n_in, self.n_out,
+                           _DTYPE_CODE[self.dtype])
+            object.__setattr__(self, "_c", c)
+        return c
 
 
 @dataclass(frozen=True)
@@ -106,9 +110,12 @@ class LayerShape:
         return self.n_routed + self.n_zero
 
     def c(self) -> MoEConfig:
-        code = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}[self.act_dtype]
-        return MoEConfig(self.T, self.d, self.n_routed, self.n_zero, self.top_k,
-                         self.ffn, code, float(self.routed_scale))
+        c = self.__dict__.get("_c")  # built once: a frozen shape does not change
+        if c is None:
+            c = MoEConfig(self.T, self.d, self.n_routed, self.n_zero, self.top_k, self.ffn,
+                          _DTYPE_CODE[self.act_dtype], float(self.routed_scale))
+            object.__setattr__(self, "_c", c)
+        return c
 
 
 _lib = None
@@ -174,7 +181,7 @@ def lib():
 
 
 def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream=None):
@@ -192,6 +199,9 @@ def _need(t: torch.Tensor, name: str, dtype, shape=None, on_device=True):
     """Checks one tensor argument before its address goes to the library. A
     host tensor where device memory is expected (or the reverse) would be
     dereferenced by a kernel or a copy on the wrong side, so it is refused."""
+    if (t.dtype == dtype and t.is_cuda == on_device and t.is_contiguous()
+            and (shape is None or t.shape == shape)):
+        return
     if t.dtype != dtype:
         raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
     if on_device and not t.is_cuda:

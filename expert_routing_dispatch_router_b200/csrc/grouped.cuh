@@ -70,8 +70,7 @@ struct BackwardWs {   // byte offsets from the workspace's base
   size_t dy_perm;     // act [T*k, d]  (whole-layer call)
   size_t dx_perm;     // act [T*k, d]  (whole-layer call)
   size_t dgate;       // float [T, k]  (whole-layer call)
-  size_t dlogit;      // float [T, k]
-  size_t dl_row;      // float [T*k]: dlogit in the order of the slot list
+  size_t dl_row;      // float [T*k]: the logits' gradients in the slot list's order
   size_t chunk_base;  // int32 [nchunks, E]
   size_t counts;      // int32 [E + 1]: slot counts, then the first chunk per expert
   size_t offsets;     // int32 [E + 1]: slots per expert, zero experts included

@@ -204,31 +204,39 @@ __global__ void __launch_bounds__(256)
 }
 
 // --------------------------------------------------- input and router grads --
-// dlogit[t, j] of every slot, also in the order of the slot list (dl_row): the
-// list holds the slots of every expert, zero experts included, by expert and
-// token. One warp per token; an invalid slot (row -1) has no gradient.
-__global__ void __launch_bounds__(256)
-    gate_backward_kernel(const float* __restrict__ gate, const float* __restrict__ dgate,
-                         const int32_t* __restrict__ list_row, int64_t T, int k,
-                         float* __restrict__ dlogit, float* __restrict__ dl_row) {
-  griddep_wait();
-  griddep_launch_dependents();
-  const int64_t t = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+// A token's slots, one per lane (lanes < k): the row of dx_perm (-1: none), the
+// router row, the gate of a zero-expert slot (else 0), and the gradient of the
+// slot's logit, dl = gate (dgate - sum gate dgate). A slot with an id outside
+// [0, E) has none of them.
+struct Slot {
+  int row, e;
+  float zero, dl;
+};
+__device__ __forceinline__ Slot load_slot(const int32_t* __restrict__ idx,
+                                          const float* __restrict__ gate,
+                                          const float* __restrict__ dgate,
+                                          const int32_t* __restrict__ slot_row, int64_t t, int N,
+                                          int E, int k, int64_t rows) {
   const int lane = threadIdx.x & 31;
-  if (t >= T) return;
+  Slot s{-1, 0, 0.f, 0.f};
   float g = 0.f, dg = 0.f;
-  int r = -1;
+  int e = -1, r = -1;
   if (lane < k) {
+    e = idx[t * k + lane];
+    r = slot_row[t * k + lane];
     g = gate[t * k + lane];
     dg = dgate[t * k + lane];
-    r = list_row[t * k + lane];
   }
   const float mean = sum_warp(g * dg);
-  if (lane < k) {
-    const float dl = r >= 0 ? g * (dg - mean) : 0.f;
-    dlogit[t * k + lane] = dl;
-    if (r >= 0) dl_row[r] = dl;
+  if (e >= 0 && e < E) {
+    s.e = e;
+    s.dl = g * (dg - mean);
+    if (e >= N)
+      s.zero = g;
+    else if (r >= 0 && r < rows)
+      s.row = r;
   }
+  return s;
 }
 
 constexpr int kDwChunk = 128;   // slots per partial sum of the router gradient
@@ -317,14 +325,16 @@ __global__ void __launch_bounds__(256)
   store4(dw + (int64_t)e * d + col, v);
 }
 
-// dx[t, :], one block per token and 128 vectors of columns.
+// dx[t, :], one block per token and 128 vectors of columns. The first block of a
+// token also puts the slots' dl into the order of the slot list.
 template <typename AT>
 __global__ void __launch_bounds__(128)
     input_dx_kernel(const AT* __restrict__ dout, const AT* __restrict__ dx_perm,
                     const float* __restrict__ w_router, const int32_t* __restrict__ idx,
-                    const float* __restrict__ gate, const int32_t* __restrict__ slot_row,
-                    const float* __restrict__ dlogit, AT* __restrict__ dx, int64_t d, int N,
-                    int E, int k, int64_t rows) {
+                    const float* __restrict__ gate, const float* __restrict__ dgate,
+                    const int32_t* __restrict__ slot_row, const int32_t* __restrict__ list_row,
+                    float* __restrict__ dl_row, AT* __restrict__ dx, int64_t d, int N, int E,
+                    int k, int64_t rows) {
   constexpr int V = Chunk<AT>::n;
   __shared__ int32_t s_row[kMaxTopK], s_e[kMaxTopK];
   __shared__ float s_dl[kMaxTopK], s_zero[kMaxTopK];
@@ -332,14 +342,16 @@ __global__ void __launch_bounds__(128)
   griddep_launch_dependents();
   const int64_t t = blockIdx.x;
   const int64_t col = ((int64_t)blockIdx.y * blockDim.x + threadIdx.x) * V;
-  if ((int)threadIdx.x < k) {
-    const int e = idx[t * k + threadIdx.x];
-    const int r = slot_row[t * k + threadIdx.x];
-    const bool ok = e >= 0 && e < E;
-    s_row[threadIdx.x] = ok && e < N && r >= 0 && r < rows ? r : -1;
-    s_e[threadIdx.x] = ok ? e : 0;
-    s_dl[threadIdx.x] = ok ? dlogit[t * k + threadIdx.x] : 0.f;
-    s_zero[threadIdx.x] = ok && e >= N ? gate[t * k + threadIdx.x] : 0.f;
+  if (threadIdx.x < 32) {
+    const Slot s = load_slot(idx, gate, dgate, slot_row, t, N, E, k, rows);
+    if ((int)threadIdx.x < k) {
+      s_row[threadIdx.x] = s.row;
+      s_e[threadIdx.x] = s.e;
+      s_dl[threadIdx.x] = s.dl;
+      s_zero[threadIdx.x] = s.zero;
+      const int r = blockIdx.y == 0 ? list_row[t * k + threadIdx.x] : -1;
+      if (r >= 0 && r < rows) dl_row[r] = s.dl;
+    }
   }
   Chunk<AT> g;
   if (col < d)
@@ -372,7 +384,7 @@ __global__ void __launch_bounds__(128)
     zero += s_zero[j];
     any_zero |= s_e[j] >= N;
   }
-  if (any_zero) {
+  if (any_zero) {  // a token without zero experts does not see dout here
 #pragma unroll
     for (int i = 0; i < V; ++i) acc[i] = fmaf(zero, g.get(i), acc[i]);
   }
@@ -425,15 +437,20 @@ cudaError_t input_backward(const Shape& sh, const BackwardWs& L, const void* dou
   int32_t* offsets = at<int32_t>(ws, L.offsets);
   int32_t* list_row = at<int32_t>(ws, L.slot_row);
   int32_t* token = at<int32_t>(ws, L.row_token);
-  float* dlogit = at<float>(ws, L.dlogit);
   float* dl_row = at<float>(ws, L.dl_row);
   float* part = at<float>(ws, L.dw_part);
   int32_t* counts = at<int32_t>(ws, L.counts);
   cudaError_t e = launch_dispatch(all, x, idx, at<int32_t>(ws, L.chunk_base), counts, offsets,
                                   token, list_row, nullptr, at<int32_t>(ws, L.header), st);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(gate_backward_kernel, dim3((unsigned)((sh.T + 7) / 8)), dim3(256), 0, st, gate,
-                 dgate, static_cast<const int32_t*>(list_row), sh.T, (int)sh.k, dlogit, dl_row);
+  const AT *go = static_cast<const AT*>(dout), *gp = static_cast<const AT*>(dx_perm);
+  AT* gx = static_cast<AT*>(dx);
+  const int64_t slots = sh.T * sh.k;
+  e = launch_pdl(input_dx_kernel<AT>,
+                 dim3((unsigned)sh.T, (unsigned)((sh.d + 128 * V - 1) / (128 * V))), dim3(128),
+                 0, st, go, gp, w_router, idx, gate, dgate, slot_row,
+                 static_cast<const int32_t*>(list_row), dl_row, gx, sh.d, (int)sh.N, (int)sh.E,
+                 (int)sh.k, slots);
   if (e != cudaSuccess) return e;
   const int64_t cb = (sh.d + kDwThreads * V - 1) / (kDwThreads * V);
   int64_t blocks = router_dw_chunks(sh) * cb;
@@ -444,16 +461,10 @@ cudaError_t input_backward(const Shape& sh, const BackwardWs& L, const void* dou
                  static_cast<const int32_t*>(token), static_cast<const float*>(dl_row),
                  (int)sh.E, sh.T * sh.k, sh.d, part, counts);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(router_dw_sum_kernel, dim3((unsigned)sh.E, (unsigned)((sh.d + 1023) / 1024)),
-                 dim3(256), 0, st, static_cast<const float*>(part),
-                 static_cast<const int32_t*>(counts), sh.d, dw_router);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(input_dx_kernel<AT>,
-                    dim3((unsigned)sh.T, (unsigned)((sh.d + 128 * V - 1) / (128 * V))),
-                    dim3(128), 0, st, static_cast<const AT*>(dout),
-                    static_cast<const AT*>(dx_perm), w_router, idx, gate, slot_row,
-                    static_cast<const float*>(dlogit), static_cast<AT*>(dx), sh.d, (int)sh.N,
-                    (int)sh.E, (int)sh.k, sh.T * sh.k);
+  return launch_pdl(router_dw_sum_kernel,
+                    dim3((unsigned)sh.E, (unsigned)((sh.d + 1023) / 1024)), dim3(256), 0, st,
+                    static_cast<const float*>(part), static_cast<const int32_t*>(counts), sh.d,
+                    dw_router);
 }
 
 cudaError_t swiglu_backward(const Shape& sh, const float* dh, const int32_t* offsets, void* h,
@@ -488,7 +499,6 @@ BackwardWs backward_ws(const Shape& sh) {
   L.dy_perm = take(routed ? Tk * sh.d * act : 0);
   L.dx_perm = take(routed ? Tk * sh.d * act : 0);
   L.dgate = take(Tk * 4);
-  L.dlogit = take(Tk * 4);
   L.dl_row = take(Tk * 4);
   L.chunk_base = take((size_t)sh.nchunks * sh.E * 4);
   L.counts = take((size_t)(sh.E + 1) * 4);

@@ -179,7 +179,8 @@ def test_expert_ffn_backward_fp32_gradients_and_hot_expert():
 LAYER = [dict(T=1, d=64, N=3, Z=1, k=2), dict(T=37, d=72, N=5, Z=3, k=4),
          dict(T=20, d=520, N=0, Z=4, k=3), dict(T=65, d=136, N=40, Z=0, k=12),
          dict(T=12, d=4104, N=30, Z=10, k=32), dict(T=300, d=64, N=4, Z=2, k=1),
-         dict(T=1500, d=72, N=3, Z=2, k=3)]
+         dict(T=1500, d=72, N=3, Z=2, k=3), dict(T=2100, d=136, N=5, Z=2, k=3),
+         dict(T=2049, d=520, N=0, Z=9, k=9)]
 IDS = lambda c: "-".join(str(v) for v in c.values())  # noqa: E731
 
 
