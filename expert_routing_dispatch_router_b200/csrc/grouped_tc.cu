@@ -196,10 +196,10 @@ __device__ __forceinline__ void mma_stage(uint32_t d, uint64_t a, uint64_t b, ui
         : "memory");
 }
 
-// Arrive on another CTA's mbarrier where nothing in memory passes to it (an
-// accumulator has been read, a ring slot taken): release at CTA scope. At
-// cluster scope the arrive would first wait for every store this warp has in
-// flight.
+// Arrive on another CTA's mbarrier where nothing in memory passes to it: an
+// accumulator has been read, which tcgen05.wait::ld has completed before. Release
+// at CTA scope; at cluster scope the arrive would first wait for every store this
+// warp has in flight.
 __device__ __forceinline__ void mbar_arrive_remote_light(uint32_t cluster_bar) {
   asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar)
                : "memory");
@@ -330,10 +330,14 @@ constexpr uint32_t kCtlBytes = 320;
 // counter in the workspace, so CTAs whose units were short take more of them.
 // The (leader's) producer publishes each unit id, -1 at the end, in a ring of
 // kRing slots in its own and its peer's shared memory; the other roles read
-// their units from there. A slot is free again when its readers have arrived on
-// the publisher's ring_empty: the MMA warp, the epilogue warps, a second
-// producer if there is one (TWO) and, in a pair, the peer's producers and
-// epilogue warps. The last CTA (pair) to finish returns the counters to zero.
+// their units from there and arrive on the ring_empty barrier of their own CTA:
+// the MMA warp, the epilogue warps, a second producer if there is one (TWO), and
+// in the peer its producers and epilogue warps. A thread of the peer's otherwise
+// idle warp 1 passes the peer's takes on to the leader at cluster scope, so a
+// slot is stored to again only after everyone has read it. (Each reader could
+// arrive there itself; at cluster scope it would first wait for its stores in
+// flight, and at a narrower one its read would not be ordered before the next
+// store to the slot.) The last CTA (pair) to finish returns the counters to zero.
 template <int S, bool PAIR, bool TWO>
 struct Control {
   uint32_t bars;
@@ -347,7 +351,9 @@ struct Control {
   __device__ bool publish(int seq, int u, int32_t* err) const {
     const int r = seq % kRing;
     const uint32_t par = (uint32_t)(seq / kRing) & 1u;
-    if (!wait_bounded(ring_empty(r), par ^ 1u, abort_flag, err)) return false;
+    if (PAIR ? !wait_bounded_cluster(ring_empty(r), par ^ 1u, abort_flag, err)
+             : !wait_bounded(ring_empty(r), par ^ 1u, abort_flag, err))
+      return false;
     ring[r] = u;
     if (PAIR) {
       ptx::st_shared_cluster_u32(
@@ -364,11 +370,21 @@ struct Control {
              : !wait_bounded(ring_full(r), par, abort_flag, err))
       return false;
     *u = ring[r];
-    if (PAIR && Cg<PAIR>::rank() != 0)
-      mbar_arrive_remote_light(ptx::map_to_rank(ring_empty(r), 0));
-    else
-      ptx::mbar_arrive(ring_empty(r));
+    ptx::mbar_arrive(ring_empty(r));
     return true;
+  }
+  // The peer's warp 1 (one lane): once all of the peer has taken a unit, say so
+  // to the leader.
+  __device__ void relay_takes(int32_t* err) const {
+    for (int seq = 0;; ++seq) {
+      const int r = seq % kRing;
+      const uint32_t par = (uint32_t)(seq / kRing) & 1u;
+      if (!wait_bounded_cluster(ring_full(r), par, abort_flag, err)) return;
+      const int u = ring[r];
+      if (!wait_bounded(ring_empty(r), par, abort_flag, err)) return;
+      ptx::mbar_arrive_remote(ptx::map_to_rank(ring_empty(r), 0));
+      if (u < 0) return;
+    }
   }
   // Next unit for the producer warp: the leader publishes the one it claimed
   // before, then claims another (after the arrivals, which would wait for the
@@ -420,7 +436,10 @@ struct Control {
       ptx::mbar_init(mma_done(), 1);
       for (int r = 0; r < kRing; ++r) {
         ptx::mbar_init(ring_full(r), 1);
-        ptx::mbar_init(ring_empty(r), (1 + kEpiWarps + TWO) * (PAIR ? 2 : 1));
+        // leader: MMA warp, epilogue, second producer, relay; peer: producer,
+        // epilogue, second producer
+        ptx::mbar_init(ring_empty(r),
+                       1 + kEpiWarps + TWO + (PAIR && Cg<PAIR>::rank() == 0 ? 1 : 0));
       }
       *abort_flag = 0;
       ptx::fence_mbar_init();
@@ -713,6 +732,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         G::commit(ctl.mma_done());
         wait_cleanup(ctl.mma_done(), 0);
       }
+      __syncwarp();
+    } else {
+      if (lane == 0) ctl.relay_takes(args.err);
       __syncwarp();
     }
   } else {
@@ -1110,6 +1132,9 @@ __global__ void __launch_bounds__(kDwThreads, 1)
         G::commit(ctl.mma_done());
         wait_cleanup(ctl.mma_done(), 0);
       }
+      __syncwarp();
+    } else {
+      if (lane == 0) ctl.relay_takes(args.err);
       __syncwarp();
     }
   } else {

@@ -359,6 +359,27 @@ def test_results_do_not_change_from_run_to_run_or_with_the_stream():
         assert torch.equal(a, b) and torch.equal(a, c)
 
 
+@pytest.mark.parametrize("sizes", [(900, 0, 1700, 330, 20, 64, 321, 257), (300,) * 24],
+                         ids=["skewed", "even"])
+def test_many_units_and_runs_give_the_same_result(sizes):
+    # hundreds of work units per launch handed from CTA pair to CTA pair, of
+    # one and of several tiles: every run equals the first bit for bit
+    R, N, d, F = sum(sizes), len(sizes), 1024, 1024
+    g = torch.Generator(device=DEV).manual_seed(34)
+    mk = lambda *s, sc=1.0: (torch.randn(*s, generator=g, device=DEV) * sc).to(BF)  # noqa: E731
+    off = dev(ref.offsets_of(sizes))
+    sh = moe.LayerShape(R, d, N, 1, 1, F, BF)
+    ws = moe.alloc_backward_workspace(sh)
+    x, dy = mk(R, d), mk(R, d)
+    wg, wu, wd = (mk(*s, sc=d ** -0.5) for s in ((N, F, d), (N, F, d), (N, d, F)))
+    first = moe.expert_ffn_backward(sh, x, off, wg, wu, wd, dy, ws)
+    again = [torch.empty_like(t) for t in first]
+    for run in range(40):
+        moe.expert_ffn_backward(sh, x, off, wg, wu, wd, dy, ws, *again)
+        assert all(torch.equal(a, b) for a, b in zip(first, again)), run
+    assert moe.read_device_error(ws) == 0
+
+
 def test_empty_batch_gives_zero_weight_gradients():
     ls = moe.LayerShape(0, 64, 2, 1, 2, 32, BF)
     e = lambda *s, dt=BF: torch.empty(*s, dtype=dt, device=DEV)  # noqa: E731
