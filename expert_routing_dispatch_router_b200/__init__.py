@@ -185,9 +185,9 @@ def _ptr(t: Optional[torch.Tensor]):
 
 
 def _stream(stream=None):
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+    if stream is None:  # the handle alone: the Stream object costs 3.5 us
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream
 
 
 def _check(fn: str, status: int):
@@ -490,6 +490,15 @@ def bias_pid_update(shape: LayerShape, counts, bias, state, target: float, kp: f
 
 
 # ------------------------------------------------------------------ training --
+def _on_current_device(*tensors):
+    """Refuses tensors of another device than the current one, whose kernels
+    could not read them."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"a tensor is on {t.device}, but the current device is cuda:{dev}")
+
+
 def alloc_grouped_workspace(shape: GroupedShape, device="cuda") -> torch.Tensor:
     """Zeroed workspace of the grouped products (the error word and counters)."""
     n = int(lib().moe_grouped_workspace_size(ctypes.byref(shape.c())))
@@ -515,6 +524,7 @@ def grouped_matmul(shape: GroupedShape, x, w, offsets, ws, out=None, stream=None
     _need(w, "w", shape.dtype, (G, O, I))
     _need(offsets, "offsets", torch.int32, (G + 1,))
     out = _out(out, "out", shape.dtype, (R, O), x.device)
+    _on_current_device(x, w, offsets, ws, out)
     st = lib().moe_grouped_matmul(ctypes.byref(shape.c()), _ptr(x), _ptr(w), _ptr(offsets),
                                   _ptr(out), *_ws(ws), _stream(stream))
     _check("moe_grouped_matmul", st)
@@ -529,6 +539,7 @@ def grouped_matmul_dx(shape: GroupedShape, dy, w, offsets, ws, out=None, stream=
     _need(w, "w", shape.dtype, (G, O, I))
     _need(offsets, "offsets", torch.int32, (G + 1,))
     out = _out(out, "out", shape.dtype, (R, I), dy.device)
+    _on_current_device(dy, w, offsets, ws, out)
     st = lib().moe_grouped_matmul_dx(ctypes.byref(shape.c()), _ptr(dy), _ptr(w),
                                      _ptr(offsets), _ptr(out), *_ws(ws), _stream(stream))
     _check("moe_grouped_matmul_dx", st)
@@ -545,6 +556,7 @@ def grouped_matmul_dw(shape: GroupedShape, dy, x, offsets, ws, out=None, stream=
     _need(offsets, "offsets", torch.int32, (G + 1,))
     f32 = out is not None and out.dtype == torch.float32
     out = _out(out, "out", torch.float32 if f32 else shape.dtype, (G, O, I), x.device)
+    _on_current_device(dy, x, offsets, ws, out)
     st = lib().moe_grouped_matmul_dw(ctypes.byref(shape.c()), _ptr(dy), _ptr(x),
                                      _ptr(offsets), _ptr(out), _DTYPE_CODE[out.dtype],
                                      *_ws(ws), _stream(stream))
@@ -576,6 +588,7 @@ def combine_backward(shape: LayerShape, dout, x, y_perm, topk_idx, topk_gate, sl
     _need(slot_row, "slot_row", torch.int32, (T * k,))
     dy_perm = _out(dy_perm, "dy_perm", shape.act_dtype, (T * k, d), x.device)
     dgate = _out(dgate, "dgate", torch.float32, (T, k), x.device)
+    _on_current_device(dout, x, y_perm, topk_idx, topk_gate, slot_row, dy_perm, dgate)
     st = lib().moe_combine_backward(ctypes.byref(shape.c()), _ptr(dout), _ptr(x),
                                     _ptr(y_perm), _ptr(topk_idx), _ptr(topk_gate),
                                     _ptr(slot_row), _ptr(dy_perm), _ptr(dgate),
@@ -619,6 +632,7 @@ def expert_ffn_backward(shape: LayerShape, x_perm, offsets, w_gate, w_up, w_down
     _need(dy_perm, "dy_perm", shape.act_dtype, (T * k, d))
     dx_perm = _out(dx_perm, "dx_perm", shape.act_dtype, (T * k, d), x_perm.device)
     dws, code = _weight_grads(shape, dw_gate, dw_up, dw_down, x_perm.device)
+    _on_current_device(x_perm, offsets, w_gate, w_up, w_down, dy_perm, ws, dx_perm, *dws)
     st = lib().moe_expert_ffn_backward(ctypes.byref(shape.c()), _ptr(x_perm), _ptr(offsets),
                                        _ptr(w_gate), _ptr(w_up), _ptr(w_down), _ptr(dy_perm),
                                        _ptr(dx_perm), *[_ptr(t) for t in dws], code,
@@ -642,6 +656,8 @@ def input_backward(shape: LayerShape, dout, x, w_router, topk_idx, topk_gate, sl
     _need(dx_perm, "dx_perm", shape.act_dtype, (T * k, d))
     dx = _out(dx, "dx", shape.act_dtype, (T, d), x.device)
     dw_router = _out(dw_router, "dw_router", torch.float32, (E, d), x.device)
+    _on_current_device(dout, x, w_router, topk_idx, topk_gate, slot_row, dgate, dx_perm,
+                       ws, dx, dw_router)
     st = lib().moe_input_backward(ctypes.byref(shape.c()), _ptr(dout), _ptr(x),
                                   _ptr(w_router), _ptr(topk_idx), _ptr(topk_gate),
                                   _ptr(slot_row), _ptr(dgate), _ptr(dx_perm), _ptr(dx),
@@ -672,6 +688,8 @@ def layer_backward(shape: LayerShape, dout, x, w_router, w_gate, w_up, w_down, t
     dx = _out(dx, "dx", shape.act_dtype, (T, d), x.device)
     dw_router = _out(dw_router, "dw_router", torch.float32, (E, d), x.device)
     dws, code = _weight_grads(shape, dw_gate, dw_up, dw_down, x.device)
+    _on_current_device(dout, x, w_router, w_gate, w_up, w_down, topk_idx, topk_gate, offsets,
+                       slot_row, x_perm, y_perm, ws, dx, dw_router, *dws)
     st = lib().moe_layer_backward(ctypes.byref(shape.c()), _ptr(dout), _ptr(x),
                                   _ptr(w_router), _ptr(w_gate), _ptr(w_up), _ptr(w_down),
                                   _ptr(topk_idx), _ptr(topk_gate), _ptr(offsets),
@@ -779,6 +797,7 @@ def adamw_step(opt: AdamW, lr: float, beta1: float = 0.9, beta2: float = 0.999,
     hyper = MoEAdamWParams(lr, beta1, beta2, eps, weight_decay)
     m, ms = opt.m if opt.state_bits == 8 else (opt.m, None)
     v, vs = opt.v if opt.state_bits == 8 else (opt.v, None)
+    _on_current_device(opt._table)
     st = lib().moe_adamw_step(ctypes.byref(opt._c), ctypes.byref(hyper), _ptr(opt._table),
                               _ptr(m), _ptr(ms), _ptr(v), _ptr(vs), _ptr(opt.state),
                               _stream(stream))

@@ -281,6 +281,7 @@ def test_binding_calls_reach_the_library_with_an_empty_batch(monkeypatch):
     monkeypatch.setattr(moe, "_need", lambda t, n, dt, shape=None, on_device=True:
                         real(t, n, dt, shape, on_device=False))
     monkeypatch.setattr(moe, "_ws", lambda ws: (P(ws.data_ptr()), ws.numel()))
+    monkeypatch.setattr(moe, "_on_current_device", lambda *tensors: None)
     st = types.SimpleNamespace(cuda_stream=0)
     bf = torch.bfloat16
     sh = moe.LayerShape(T=0, d=64, n_routed=2, n_zero=1, top_k=2, ffn=64)
@@ -296,3 +297,13 @@ def test_binding_calls_reach_the_library_with_an_empty_batch(monkeypatch):
                               stream=st).shape == (0, 8)
     assert moe.grouped_matmul_dx(gs, torch.zeros(0, 8, dtype=bf), w, off, ws,
                                  stream=st).shape == (0, 16)
+
+
+def test_tensors_of_another_device_are_refused(monkeypatch):
+    import types
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    here, there = (types.SimpleNamespace(get_device=lambda d=d: d, device=f"cuda:{d}")
+                   for d in (1, 0))
+    moe._on_current_device(here, None, here)
+    with pytest.raises(ValueError, match="cuda:0"):
+        moe._on_current_device(here, there)
