@@ -566,6 +566,27 @@ __device__ __forceinline__ float sigmoid_f(float z) {
   return __fdividef(1.0f, 1.0f + __expf(-z));
 }
 
+// Stores 2 N rows of one column per lane: w[i] holds rows 2 i (low half) and
+// 2 i + 1 of the lane's column. Lanes exchange halves in pairs, so that an even
+// lane has row 2 i of two columns and an odd lane row 2 i + 1, and one 4-byte
+// store per pair of rows writes both. out points at row 0 of the lane's column;
+// rows from n on are not written (n differs between lanes of columns that exist
+// and lanes of columns that do not, never within a pair).
+template <int N>
+__device__ __forceinline__ void store_row_pairs(const uint32_t (&w)[N], uint16_t* out,
+                                                int64_t cols, int n) {
+  const int odd = threadIdx.x & 1;
+  uint16_t* p = out - odd + odd * cols;
+  const uint32_t pick = odd ? 0x3276 : 0x5410;  // (other hi, own hi) or (own lo, other lo)
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const uint32_t other = __shfl_xor_sync(0xffffffffu, w[i], 1);
+    const uint32_t v = __byte_perm(w[i], other, pick);
+    if (2 * i + odd < n) *reinterpret_cast<uint32_t*>(p) = v;
+    p += 2 * cols;
+  }
+}
+
 template <Mode MODE, int BN_, bool PAIR_>
 __global__ void __launch_bounds__(kThreads, 1)
     row_gemm_kernel(const __grid_constant__ RowMaps maps, const RowArgs args) {
@@ -765,12 +786,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto half_row = [&](int i) { return 64 * (i >> 1) + r0 + 16 * (i & 1); };
         float a[16], v[16];
         auto fetch = [&](int i) {
+          const int left = n_out - half_row(i);
+          const float* pa = args.pre[0] + obase + (int64_t)half_row(i) * args.cols;
+          const float* pv = args.pre[1] + obase + (int64_t)half_row(i) * args.cols;
 #pragma unroll
           for (int c = 0; c < 16; ++c) {
-            const int r = half_row(i) + c;
-            const int64_t at = obase + (int64_t)r * args.cols;
-            a[c] = r < n_out ? __ldg(args.pre[0] + at) : 0.f;
-            v[c] = r < n_out ? __ldg(args.pre[1] + at) : 0.f;
+            a[c] = c < left ? __ldg(pa) : 0.f;
+            v[c] = c < left ? __ldg(pv) : 0.f;
+            pa += args.cols;
+            pv += args.cols;
           }
         };
         if (MODE == Mode::kSwiglu) fetch(0);  // while the unit's products still run
@@ -808,19 +832,11 @@ __global__ void __launch_bounds__(kThreads, 1)
               du2[c] = *reinterpret_cast<const uint32_t*>(&zb);
             }
             if (i + 1 < halves) fetch(i + 1);
-            uint16_t* h = static_cast<uint16_t*>(args.out[0]) + obase;
-            uint16_t* da = static_cast<uint16_t*>(args.out[1]) + obase;
-            uint16_t* du = static_cast<uint16_t*>(args.out[2]) + obase;
-#pragma unroll
-            for (int c = 0; c < 16; ++c) {
-              const int r = half_row(i) + c;
-              if (r < n_out) {
-                const int64_t at = (int64_t)r * args.cols;
-                h[at] = (uint16_t)((c & 1) ? h2[c >> 1] >> 16 : h2[c >> 1]);
-                da[at] = (uint16_t)((c & 1) ? da2[c >> 1] >> 16 : da2[c >> 1]);
-                du[at] = (uint16_t)((c & 1) ? du2[c >> 1] >> 16 : du2[c >> 1]);
-              }
-            }
+            const int64_t at = obase + (int64_t)half_row(i) * args.cols;
+            const int left = n_out - half_row(i);
+            store_row_pairs(h2, static_cast<uint16_t*>(args.out[0]) + at, args.cols, left);
+            store_row_pairs(da2, static_cast<uint16_t*>(args.out[1]) + at, args.cols, left);
+            store_row_pairs(du2, static_cast<uint16_t*>(args.out[2]) + at, args.cols, left);
           }
         } else {
           // the whole share leaves TMEM before anything is stored, so the next
@@ -848,17 +864,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int q = 0; q < NQ; ++q) {
             if (64 * q + r0 < n_rows) {
+              const int64_t at = obase + (int64_t)(64 * q + r0) * args.cols;
+              const int left = n_out - 64 * q - r0;
+              if (F32) {
+                uint32_t* p = static_cast<uint32_t*>(job ? args.out[1] : args.out[0]) + at;
 #pragma unroll
-              for (int c = 0; c < 32; ++c) {
-                const int r = 64 * q + r0 + c;
-                if (r < n_out) {
-                  const int64_t at = obase + (int64_t)r * args.cols;
-                  if (F32)
-                    static_cast<uint32_t*>(job ? args.out[1] : args.out[0])[at] = w[q][c % kPer];
-                  else
-                    static_cast<uint16_t*>(args.out[0])[at] =
-                        (uint16_t)((c & 1) ? w[q][c / 2 % kPer] >> 16 : w[q][c / 2 % kPer]);
+                for (int c = 0; c < 32; ++c) {
+                  if (c < left) *p = w[q][c % kPer];
+                  p += args.cols;
                 }
+              } else {
+                store_row_pairs(w[q], static_cast<uint16_t*>(args.out[0]) + at, args.cols, left);
               }
             }
           }
