@@ -381,10 +381,10 @@ cudaError_t launch_dispatch(const Shape& sh, const void* x, const int32_t* idx,
                             int32_t* offsets, int32_t* row_token,
                             int32_t* slot_row, void* x_perm, int32_t* err,
                             cudaStream_t st, int32_t* tile_start, int tile_gu,
-                            int tile_dn) {
+                            int tile_dn, bool many_blocks) {
   const int E = (int)sh.E, N = (int)sh.N, k = (int)sh.k;
   cudaError_t e = cudaSuccess;
-  if (dispatch_small_fits(sh)) {
+  if (dispatch_small_fits(sh) && !many_blocks) {
     const int W = (int)((sh.T + 31) / 32);
     const size_t smem = dispatch_small_smem(sh);
     static std::atomic<uint64_t> attr_set{0};

@@ -423,6 +423,11 @@ T* at(void* ws, size_t off) {
 
 int64_t router_dw_chunks(const Shape& sh) { return sh.T * sh.k / kDwChunk + sh.E; }
 
+// Slots up to which the list is sorted by one block in one launch (with 320
+// experts: 6144 slots 60 against 58 us for the whole call, 12288 slots 110
+// against 86, a quarter of that 36 against 41).
+constexpr int64_t kListOneBlock = 6144;
+
 template <typename AT>
 cudaError_t input_backward(const Shape& sh, const BackwardWs& L, const void* dout,
                            const void* x, const float* w_router, const int32_t* idx,
@@ -440,8 +445,10 @@ cudaError_t input_backward(const Shape& sh, const BackwardWs& L, const void* dou
   float* dl_row = at<float>(ws, L.dl_row);
   float* part = at<float>(ws, L.dw_part);
   int32_t* counts = at<int32_t>(ws, L.counts);
-  cudaError_t e = launch_dispatch(all, x, idx, at<int32_t>(ws, L.chunk_base), counts, offsets,
-                                  token, list_row, nullptr, at<int32_t>(ws, L.header), st);
+  cudaError_t e =
+      launch_dispatch(all, x, idx, at<int32_t>(ws, L.chunk_base), counts, offsets, token,
+                      list_row, nullptr, at<int32_t>(ws, L.header), st, nullptr, 0, 0,
+                      sh.T * sh.k > kListOneBlock);
   if (e != cudaSuccess) return e;
   const AT *go = static_cast<const AT*>(dout), *gp = static_cast<const AT*>(dx_perm);
   AT* gx = static_cast<AT*>(dx);

@@ -70,12 +70,13 @@ cudaError_t launch_router(const Shape& sh, const void* x, const float* w_r,
 // x_perm null: the rows are not gathered (the gate/up GEMM gathers them).
 // tile_start given and dispatch_plans_tiles(sh): the one-block dispatch also
 // writes the expert GEMMs' token-tile prefixes for tiles tile_gu and tile_dn.
+// many_blocks: the three-kernel sort whatever the batch (same results).
 cudaError_t launch_dispatch(const Shape& sh, const void* x, const int32_t* idx,
                             int32_t* chunk_base, int32_t* counts,
                             int32_t* offsets, int32_t* row_token,
                             int32_t* slot_row, void* x_perm, int32_t* err,
                             cudaStream_t st, int32_t* tile_start = nullptr,
-                            int tile_gu = 0, int tile_dn = 0);
+                            int tile_gu = 0, int tile_dn = 0, bool many_blocks = false);
 bool dispatch_plans_tiles(const Shape& sh);
 // The one-block dispatch also gathers x_perm, in the same launch.
 bool dispatch_gathers_in_sort(const Shape& sh);

@@ -138,7 +138,8 @@ def ffn_case(T, d, N, Z, k, F, dtype, seed, popular=None):
 FFN = [dict(T=1, d=64, N=3, Z=1, k=2, F=32), dict(T=40, d=128, N=5, Z=2, k=3, F=64),
        dict(T=33, d=72, N=4, Z=0, k=1, F=40), dict(T=150, d=256, N=8, Z=2, k=2, F=384),
        dict(T=300, d=264, N=3, Z=1, k=2, F=136), dict(T=700, d=512, N=4, Z=1, k=3, F=256),
-       dict(T=64, d=64, N=2, Z=6, k=2, F=64)]
+       dict(T=64, d=64, N=2, Z=6, k=2, F=64), dict(T=5, d=8, N=2, Z=0, k=1, F=8),
+       dict(T=9, d=2048, N=3, Z=0, k=2, F=512)]
 
 
 @pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
@@ -180,7 +181,7 @@ LAYER = [dict(T=1, d=64, N=3, Z=1, k=2), dict(T=37, d=72, N=5, Z=3, k=4),
          dict(T=20, d=520, N=0, Z=4, k=3), dict(T=65, d=136, N=40, Z=0, k=12),
          dict(T=12, d=4104, N=30, Z=10, k=32), dict(T=300, d=64, N=4, Z=2, k=1),
          dict(T=1500, d=72, N=3, Z=2, k=3), dict(T=2100, d=136, N=5, Z=2, k=3),
-         dict(T=2049, d=520, N=0, Z=9, k=9)]
+         dict(T=2049, d=520, N=0, Z=9, k=9), dict(T=40, d=64, N=1000, Z=24, k=32)]
 IDS = lambda c: "-".join(str(v) for v in c.values())  # noqa: E731
 
 
@@ -398,6 +399,86 @@ def test_empty_batch_gives_zero_weight_gradients():
     dw = moe.grouped_matmul_dw(gs, e(0, 8), e(0, 16), off, moe.alloc_grouped_workspace(gs),
                                out=full(2, 8, 16))
     assert int(dw.count_nonzero()) == 0
+
+
+def test_two_calls_at_once_on_two_streams():
+    ls = moe.LayerShape(700, 512, 6, 2, 3, 512, BF, 2.0)
+    x, dout, w_r, bias, wg, wu, wd = weights(ls, 35)
+    _, idx, gate, off, slot_row, xp, yp = forward(ls, x, w_r, bias, wg, wu, wd)
+    args = (ls, dout, x, w_r, wg, wu, wd, idx, gate, off, slot_row, xp, yp)
+    spaces = [moe.alloc_backward_workspace(ls) for _ in range(3)]
+    want = moe.layer_backward(*args, spaces[2])
+    sides = [torch.cuda.Stream(), torch.cuda.Stream()]
+    outs = [[torch.empty_like(t) for t in want] for _ in sides]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for side, ws, out in zip(sides, spaces, outs):
+            moe.layer_backward(*args, ws, *out, stream=side)
+    torch.cuda.synchronize()
+    for ws, out in zip(spaces, outs):
+        assert moe.read_device_error(ws) == 0
+        assert all(torch.equal(a, b) for a, b in zip(out, want))
+
+
+# ------------------------------------------- positions behind 2^31 elements --
+def test_grouped_rows_behind_two_to_the_31():
+    R, I, O, G = 360_000, 6144, 64, 3  # x and dx hold 2.2 G elements
+    g = torch.Generator(device=DEV).manual_seed(36)
+    x = torch.randn(R, I, generator=g, device=DEV, dtype=BF)
+    dy = torch.randn(R, O, generator=g, device=DEV, dtype=BF)
+    w = torch.randn(G, O, I, generator=g, device=DEV, dtype=BF) * I ** -0.5
+    off = torch.tensor([0, 1, R - 700, R], dtype=torch.int32, device=DEV)
+    sh = moe.GroupedShape(R, G, I, O)
+    ws = moe.alloc_grouped_workspace(sh)
+    y = moe.grouped_matmul(sh, x, w, off, ws)
+    dx = moe.grouped_matmul_dx(sh, dy, w, off, ws)
+    dw = moe.grouped_matmul_dw(sh, dy, x, off, ws)
+    assert moe.read_device_error(ws) == 0
+    c = lambda t: t.double().cpu()  # noqa: E731
+    for e, lo, hi in ((0, 0, 1), (1, 200_000, 200_040), (1, R - 720, R - 700), (2, R - 700, R)):
+        ref.check(y[lo:hi], *ref.mm(c(x[lo:hi]), c(w[e]).T), BF, f"y {lo}")
+        ref.check(dx[lo:hi], *ref.mm(c(dy[lo:hi]), c(w[e])), BF, f"dx {lo}")
+    ref.check(dw[2], *ref.mm(c(dy[R - 700:]).T, c(x[R - 700:])), BF, "dw")
+
+
+def test_layer_rows_behind_two_to_the_31():
+    T, d, N, Z, k = 45_000, 6144, 8, 0, 8  # 2.2 G elements of rows
+    g = torch.Generator(device=DEV).manual_seed(37)
+    idx = torch.rand(T, N, generator=g, device=DEV).argsort(1).int()
+    gate = torch.softmax(torch.randn(T, k, generator=g, device=DEV), 1)
+    # every token chose all eight experts: row e T + t
+    slot_row = (idx.long() * T + torch.arange(T, device=DEV)[:, None]).int().view(-1)
+    mk = lambda *s: torch.randn(*s, generator=g, device=DEV, dtype=BF)  # noqa: E731
+    dout, x, rows, w_r = mk(T, d), mk(T, d), mk(T * k, d), mk(N, d).float()
+    dgate = torch.randn(T, k, generator=g, device=DEV)
+    sh = moe.LayerShape(T, d, N, Z, k, 8, BF, 1.5)
+    dy, dg = moe.combine_backward(sh, dout, x, rows, idx, gate, slot_row)
+    ws = moe.alloc_backward_workspace(sh)
+    dx, _ = moe.input_backward(sh, dout, x, w_r, idx, gate, slot_row, dgate, rows, ws)
+    assert moe.read_device_error(ws) == 0
+    pick = torch.tensor([0, 1, T // 2, T - 2, T - 1], device=DEV)
+    local = torch.arange(5 * k, dtype=torch.int32)  # the picked tokens' rows, gathered
+    at = slot_row.view(T, k)[pick].reshape(-1).long()
+    c = lambda t: t.cpu()  # noqa: E731
+    (v, ev), (gv, eg) = ref.combine_backward(c(dout[pick]), c(x[pick]), c(rows[at]), c(idx[pick]),
+                                             c(gate[pick]), local, N, 1.5)
+    ref.check(dy[at], v, ev, BF, "dy_perm")
+    ref.check(dg[pick], gv, eg, F32, "dgate")
+    want, _ = ref.input_backward(c(dout[pick]), c(x[pick]), c(w_r), c(idx[pick]), c(gate[pick]),
+                                 local, c(dgate[pick]), c(rows[at]), N)
+    ref.check(dx[pick], *want, BF, "dx")
+
+
+def test_adamw_elements_behind_two_to_the_31():
+    n = 2 ** 31 + 1000
+    p = torch.ones(n, dtype=BF, device=DEV)
+    grad = torch.zeros(n, dtype=BF, device=DEV)
+    grad[-300:], grad[:10] = 1.0, -1.0
+    opt = moe.AdamW([p], [grad], state_bits=8)
+    moe.adamw_step(opt, lr=0.25, beta1=0.5, beta2=0.5)
+    # the first step moves an element by lr in its gradient's direction
+    assert bool((p[-300:] == 0.75).all()) and bool((p[:10] == 1.25).all())
+    assert bool((p[2 ** 31 - 1000:-300] == 1.0).all()) and bool((p[10:2000] == 1.0).all())
 
 
 # ------------------------------------------------------------------ AdamW --
