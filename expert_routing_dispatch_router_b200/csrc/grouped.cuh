@@ -56,7 +56,11 @@ cudaError_t launch_swiglu_backward_tc(const GroupedShape& g, const void* x, cons
                                       float* pre_a, float* pre_u, void* h, void* da, void* du,
                                       int d, int F, const int32_t* offsets, int32_t* err,
                                       cudaStream_t st);
-// Whether unit numbers of a product fit the kernels' 32-bit counters.
+// Rows of a call. One work unit of the weight gradients is up to eight tiles over
+// all rows of a segment, about 40 ns a row; at this limit that is a third of the
+// time after which a wait for the next unit gives up.
+constexpr int64_t kMaxGroupedRows = 1ll << 24;
+// Whether a product keeps to that, and its unit numbers to 32 bits.
 bool grouped_fits(int64_t rows, int64_t groups, int64_t n_in, int64_t n_out);
 
 // ---- the experts' backward pass and the layer's other gradients ----

@@ -303,7 +303,7 @@ moe_status_t moe_bias_pid_update(const moe_config_t* cfg, const int32_t* counts,
  *  read into a result nor written. A segment without rows gives a zero dw[e].
  *  dtype is the type of every tensor but the offsets; dw_dtype may also be
  *  MOE_F32 for bf16 operands (the fp32 sums as they are).
- *  Limits: 1 <= groups <= 1024, n_in and n_out multiples of 8, and
+ *  Limits: rows <= 2^24, 1 <= groups <= 1024, n_in and n_out multiples of 8, and
  *  (rows / 64 + groups) * (max(n_in, n_out) / 64 + 1) and
  *  groups * (n_in / 64 + 1) * (n_out / 64 + 1) below 2^31.
  *  The workspace holds the error word and small counters that the kernels
@@ -332,7 +332,8 @@ moe_status_t moe_grouped_matmul_dw(const moe_grouped_t* shape, const void* dy, c
                                    void* ws, size_t ws_bytes, moe_stream_t stream);
 
 /* Bytes of workspace the backward calls of this config need (0 if cfg is
- * invalid): 256-byte aligned, its first 256 bytes zero before first use. Calls
+ * invalid; T*top_k <= 2^24 here, and the limits of the grouped products hold for
+ * d and ffn): 256-byte aligned, its first 256 bytes zero before first use. Calls
  * that share it must be ordered on one stream, as must replays of captured
  * calls that share it. */
 size_t moe_backward_workspace_size(const moe_config_t* cfg);
@@ -417,7 +418,8 @@ moe_status_t moe_layer_backward(const moe_config_t* cfg, const void* dout, const
  *         state_bits 8:  e4m3 codes of m and of sqrt(v), one byte each, with
  *         one float per block in m_scale and v_scale (value = code * scale,
  *         scale = the block's largest magnitude / 448; a positive sqrt(v)
- *         keeps at least the smallest code)
+ *         keeps at least the smallest code). A NaN or infinity in a block
+ *         reaches all of the block's 8-bit state.
  *  state  16 bytes on the device: int64 step count, then scratch. Zero at the
  *         start; each call adds one, so a captured call counts on when it is
  *         replayed.

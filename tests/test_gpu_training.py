@@ -576,6 +576,23 @@ def test_adamw_steps(sizes, pdt, gdt, master, bits):
     assert int(opt.state[0]) == 4
 
 
+def test_adamw_states_of_very_small_and_large_values():
+    # blocks whose scale or its reciprocal lies far from one, subnormal second
+    # moments among them: the 8-bit states still equal the formulas'
+    g = torch.Generator().manual_seed(43)
+    grad = ref.random(g, 4 * 256)
+    for b, size in enumerate((1e-20, 1e-30, 1e17, 1e-3)):
+        grad[256 * b:256 * (b + 1)] *= size
+    p, gd = torch.zeros(1024, device=DEV), dev(grad)
+    opt, plain = moe.AdamW([p], [gd], state_bits=8), Plain([torch.zeros(1024)], 8)
+    for _ in range(3):
+        moe.adamw_step(opt, **HYPER)
+        plain.step([grad], **HYPER)
+        for mine, want in ((opt.m, plain.qm), (opt.v, plain.qr)):
+            assert torch.equal(mine[1].cpu(), want[1])
+            assert torch.equal(mine[0].cpu().float(), want[0].float())
+
+
 @pytest.mark.parametrize("bits", [32, 8])
 def test_adamw_against_64_bits(bits):
     g = torch.Generator().manual_seed(41)

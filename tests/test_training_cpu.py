@@ -94,7 +94,7 @@ def test_grouped_shapes_refused():
     for bad, code in ((grouped(rows=-1), 1), (grouped(groups=0), 1), (grouped(n_in=0), 1),
                       (grouped(n_out=-8), 1), (grouped(dt=9), 1), (grouped(n_in=60), 2),
                       (grouped(n_out=4), 2), (grouped(groups=1025), 2),
-                      (grouped(rows=2 ** 31 - 1, n_in=65536), 2),
+                      (grouped(rows=2 ** 31 - 1, n_in=65536), 2), (grouped(rows=2 ** 24 + 1), 2),
                       (grouped(groups=1024, n_in=1 << 17, n_out=1 << 17), 2)):
         assert L.moe_grouped_workspace_size(ctypes.byref(bad)) == 0
         for fn in (L.moe_grouped_matmul, L.moe_grouped_matmul_dx):
@@ -140,7 +140,9 @@ def test_backward_configs_refused():
     n = L.moe_backward_workspace_size(ctypes.byref(cfg()))
     assert n > 0
     assert L.moe_backward_workspace_size(ctypes.byref(cfg(N=0))) > 0
+    assert L.moe_backward_workspace_size(ctypes.byref(cfg(T=2 ** 23, d=128))) > 0
     for bad, code in ((cfg(k=11), 1), (cfg(d=12), 2), (cfg(F=20), 2), (cfg(T=-1), 1),
+                      (cfg(T=2 ** 23 + 1, d=128), 2),
                       (cfg(dt=5), 1), (cfg(N=1100), 2), (cfg(s=float("nan")), 1)):
         assert L.moe_backward_workspace_size(ctypes.byref(bad)) == 0
         b = ctypes.byref(bad)
