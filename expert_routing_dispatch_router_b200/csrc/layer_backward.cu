@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(256)
 // A token's slots, one per lane (lanes < k): the row of dx_perm (-1: none), the
 // router row, the gate of a zero-expert slot (else 0), and the gradient of the
 // slot's logit, dl = gate (dgate - sum gate dgate). A slot with an id outside
-// [0, E) has none of them.
+// [0, E) has none of them (e is -1).
 struct Slot {
   int row, e;
   float zero, dl;
@@ -218,7 +218,7 @@ __device__ __forceinline__ Slot load_slot(const int32_t* __restrict__ idx,
                                           const int32_t* __restrict__ slot_row, int64_t t, int N,
                                           int E, int k, int64_t rows) {
   const int lane = threadIdx.x & 31;
-  Slot s{-1, 0, 0.f, 0.f};
+  Slot s{-1, -1, 0.f, 0.f};
   float g = 0.f, dg = 0.f;
   int e = -1, r = -1;
   if (lane < k) {
@@ -397,8 +397,9 @@ __global__ void __launch_bounds__(128)
     for (int q = 0; q < 4; ++q)
 #pragma unroll
       for (int i = 0; i < V / 4; ++i)
-        w[q][i] = j0 + q < k ? load4(w_router + (int64_t)s_e[j0 + q] * d + col + 4 * i)
-                             : make_float4(0.f, 0.f, 0.f, 0.f);
+        w[q][i] = j0 + q < k && s_e[j0 + q] >= 0
+                      ? load4(w_router + (int64_t)s_e[j0 + q] * d + col + 4 * i)
+                      : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const float dl = j0 + q < k ? s_dl[j0 + q] : 0.f;
