@@ -701,12 +701,15 @@ def layer_backward(shape: LayerShape, dout, x, w_router, w_gate, w_up, w_down, t
 
 
 ADAMW_BLOCK = 256  # elements per state block
+_DATA_PTR = torch.Tensor.data_ptr
 
 
 class AdamW:
     """The states of an AdamW optimizer over fixed weights and gradient buffers
     (step it with adamw_step). The tensors are kept alive and updated in place;
-    a step reads whatever the gradient buffers hold then.
+    a step reads whatever the gradient buffers hold then. They stay in the
+    memory they had at construction: a step refuses a weight that has moved since
+    (a replayed step cannot).
 
     params: float32 or bfloat16 CUDA tensors, one type for all; grads: tensors
     of the same sizes, one type for all. master: float32 copies of bfloat16
@@ -744,6 +747,8 @@ class AdamW:
         self.params, self.grads, self.master = params, grads, master
         self.state_bits = state_bits
         dev = params[0].device
+        self._memory = [t.detach() for t in params + grads + master if t is not None]
+        self._addresses = [p.data_ptr() for p in params]
         rows, at = [], 0
         for p, g, w in zip(params, grads, master):
             rows.append([p.data_ptr(), 0 if w is None else w.data_ptr(), g.data_ptr(),
@@ -797,6 +802,8 @@ def adamw_step(opt: AdamW, lr: float, beta1: float = 0.9, beta2: float = 0.999,
     hyper = MoEAdamWParams(lr, beta1, beta2, eps, weight_decay)
     m, ms = opt.m if opt.state_bits == 8 else (opt.m, None)
     v, vs = opt.v if opt.state_bits == 8 else (opt.v, None)
+    if list(map(_DATA_PTR, opt.params)) != opt._addresses:
+        raise ValueError("a weight has moved to other memory")
     _on_current_device(opt._table)
     st = lib().moe_adamw_step(ctypes.byref(opt._c), ctypes.byref(hyper), _ptr(opt._table),
                               _ptr(m), _ptr(ms), _ptr(v), _ptr(vs), _ptr(opt.state),

@@ -26,9 +26,10 @@
 // 8 i .. 8 i + 7, so all accesses are 8- to 16-byte vectors and the block's
 // maxima are warp reductions.
 #include <cuda_fp8.h>
+#include <float.h>
 #include <math.h>
 
-#include "moe_internal.cuh"
+#include "grouped.cuh"
 
 namespace moe {
 namespace {
@@ -206,7 +207,7 @@ __global__ void __launch_bounds__(kAdamThreads) adamw_kernel(const AdamArgs a) {
     }
     const moe_adamw_tensor_t tn = a.table[lo];
     const int64_t at = (b - tn.first_block) * kBlock + lane * 8;  // in the tensor
-    const int64_t left = tn.n - at;
+    const int64_t left = at < 0 ? 0 : tn.n - at;  // no tensor has blocks before its own
     const int n = left >= 8 ? 8 : (left > 0 ? (int)left : 0);
     const int64_t sat = b * kBlock + lane * 8;  // in the states
     float g[8], p[8], m[8], v[8], r[8];
@@ -275,16 +276,26 @@ extern "C" moe_status_t moe_adamw_step(const moe_adamw_t* opt, const moe_adamw_p
       (o.state_bits != 8 && o.state_bits != 32))
     return MOE_ERR_INVALID_ARG;
   // betas in [0, 1), finite rates; eps > 0 (0 / 0 for an element that never
-  // had a gradient)
+  // had a gradient), and with a quotient that the fast divide is good for: a
+  // normal float below 2^126, to which sqrt(v) adds at most 2^91
   if (!(h.beta1 >= 0.0 && h.beta1 < 1.0 && h.beta2 >= 0.0 && h.beta2 < 1.0) ||
       !isfinite(h.lr) || h.lr < 0.0 || !isfinite(h.weight_decay) || h.weight_decay < 0.0 ||
-      !isfinite(h.eps) || !((float)h.eps > 0.f))
+      !(h.eps >= FLT_MIN && h.eps <= 1e30))
     return MOE_ERR_INVALID_ARG;
   if (!ptr_ok(state, 15)) return MOE_ERR_INVALID_ARG;
   const bool eight = o.state_bits == 8, any = o.total_blocks > 0;
   if (any && (o.n_tensors == 0 || !ptr_ok(table, 15) || !ptr_ok(m, 15) || !ptr_ok(v, 15) ||
               (eight && (!ptr_ok(m_scale, 15) || !ptr_ok(v_scale, 15)))))
     return MOE_ERR_INVALID_ARG;
+  const size_t blocks = (size_t)o.total_blocks, codes = blocks * kBlock * (eight ? 1 : 4);
+  const size_t scales = eight ? blocks * 4 : 0;
+  const Span spans[6] = {{table, any ? o.n_tensors * sizeof(moe_adamw_tensor_t) : 0, false},
+                         {m, codes, true},
+                         {m_scale, scales, true},
+                         {v, codes, true},
+                         {v_scale, scales, true},
+                         {state, sizeof(AdamState), true}};
+  if (!disjoint(spans)) return MOE_ERR_INVALID_ARG;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   AdamState* s = static_cast<AdamState*>(state);
   cudaError_t e =

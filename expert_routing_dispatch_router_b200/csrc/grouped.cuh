@@ -101,6 +101,25 @@ cudaError_t launch_input_backward(const Shape& sh, const void* dout, const void*
                                   const void* dx_perm, void* dx, float* dw_router, void* ws,
                                   cudaStream_t st);
 
+// ---- host helpers of the entry points ----
+// A buffer of a call: outputs may share no byte with any other buffer.
+struct Span {
+  const void* p;
+  size_t bytes;
+  bool out;
+};
+template <int N>
+bool disjoint(const Span (&s)[N]) {
+  for (int i = 0; i < N; ++i)
+    for (int j = i + 1; j < N; ++j) {
+      if (!s[i].out && !s[j].out) continue;
+      const uintptr_t a = reinterpret_cast<uintptr_t>(s[i].p);
+      const uintptr_t b = reinterpret_cast<uintptr_t>(s[j].p);
+      if (s[i].bytes && s[j].bytes && a < b + s[j].bytes && b < a + s[i].bytes) return false;
+    }
+  return true;
+}
+
 // ---- device helpers ----
 // Segment table of a block in shared memory: s_off[0..n] the row offsets,
 // s_tile[0..n] the prefix sums of the segments' tiles of `tile` rows, where up

@@ -502,7 +502,7 @@ struct RowArgs {
   int groups;
   int cols;      // output columns
   int k_blocks;  // per source
-  bool wide_w;   // kDx: both 64-column blocks of a weight tile come in one copy
+  bool wide_w;   // kDx, kSwiglu: both 64-column blocks of a weight tile come in one copy
   int sources;   // 2: a second (weights, rows) pair extends the contraction
   // kFwd, kDx: out[0] bf16. kFwdF32: out[0] a, out[1] u. kSwiglu: out[0] h,
   // out[1] da, out[2] du, all bf16, from pre[0] a and pre[1] u.

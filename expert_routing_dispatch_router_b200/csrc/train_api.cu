@@ -24,24 +24,6 @@ bool dev_ok(const void* p) {
   return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 15u) == 0;
 }
 
-// A buffer of a call: outputs may share no byte with any other buffer.
-struct Span {
-  const void* p;
-  size_t bytes;
-  bool out;
-};
-template <int N>
-bool disjoint(const Span (&s)[N]) {
-  for (int i = 0; i < N; ++i)
-    for (int j = i + 1; j < N; ++j) {
-      if (!s[i].out && !s[j].out) continue;
-      const uintptr_t a = reinterpret_cast<uintptr_t>(s[i].p);
-      const uintptr_t b = reinterpret_cast<uintptr_t>(s[j].p);
-      if (s[i].bytes && s[j].bytes && a < b + s[j].bytes && b < a + s[i].bytes) return false;
-    }
-  return true;
-}
-
 moe_status_t cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
 
 constexpr size_t kGroupedWs = 256;  // the error word and unit counters

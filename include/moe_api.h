@@ -424,8 +424,9 @@ moe_status_t moe_layer_backward(const moe_config_t* cfg, const void* dout, const
  *         start; each call adds one, so a captured call counts on when it is
  *         replayed.
  *  Returns MOE_ERR_INVALID_ARG for a beta outside [0, 1), a negative or
- *  non-finite lr or weight_decay, an eps that is not positive, or a bad
- *  pointer. Host structs are read during the call only. */
+ *  non-finite lr or weight_decay, an eps outside [2^-126, 1e30], a bad
+ *  pointer, or overlapping states. What the table points to cannot be checked
+ *  here: weights and masters may overlap nothing else. Host structs are read during the call only. */
 typedef struct {
   void* param;
   float* master; /* NULL: param itself is updated */

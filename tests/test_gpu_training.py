@@ -235,7 +235,6 @@ def test_invalid_ids_stay_in_bounds_and_are_reported():
     rows = torch.where(rows.isnan(), 0.0, rows).to(BF)
     idx[3, 1], idx[7, 0] = 99, -4
     slot_row.view(50, 3)[3, 1] = slot_row.view(50, 3)[7, 0] = -1
-    routed = torch.nonzero(idx[20] < 4).flatten()
     sh = moe.LayerShape(50, 64, 4, 2, 3, 8, BF)
     ws = moe.alloc_backward_workspace(sh)
     a = dev(dout, x, rows, idx, gate, slot_row)
@@ -244,7 +243,22 @@ def test_invalid_ids_stay_in_bounds_and_are_reported():
     dx, _ = moe.input_backward(sh, a[0], a[1], dev(w_r), a[3], a[4], a[5], dev(dgate), a[2], ws)
     assert moe.read_device_error(ws) == 2
     assert moe.read_device_error(ws) == 0
-    assert bool(torch.isfinite(dx).all()) and routed is not None
+    assert bool(torch.isfinite(dx).all())
+
+
+def test_a_slot_with_an_invalid_id_adds_no_router_row():
+    # not even zero times a row that holds no number
+    c = dict(T=50, d=64, N=4, Z=2, k=3)
+    idx, gate, slot_row, off, dout, x, rows, w_r, dgate = layer_case(c, BF, 23)
+    rows = torch.where(rows.isnan(), 0.0, rows).to(BF)
+    idx[5] = torch.tensor([1, -1, 2])
+    slot_row.view(50, 3)[5] = torch.tensor([0, -1, 1])
+    w_r[0] = float("nan")
+    sh = moe.LayerShape(50, 64, 4, 2, 3, 8, BF)
+    ws = moe.alloc_backward_workspace(sh)
+    dx, _ = moe.input_backward(sh, *dev(dout, x, w_r, idx, gate, slot_row, dgate, rows), ws)
+    assert moe.read_device_error(ws) == 2
+    assert bool(torch.isfinite(dx[5]).all())
 
 
 # ------------------------------------------------------------ whole layer --
@@ -621,6 +635,33 @@ def test_adamw_against_64_bits(bits):
     scale = upd.abs() / m64.abs().clamp(min=1e-30)
     tol = h["lr"] * (scale * m_err + 16 * ref.U * upd.abs()) + 2 * ref.U * p.abs().double()
     assert bool(((pd.cpu().double() - want).abs() <= tol).all())
+
+
+def test_adamw_refuses_weights_that_moved():
+    p, grad = torch.ones(300, device=DEV), torch.ones(300, device=DEV)
+    opt = moe.AdamW([p], [grad])
+    memory = grad.data_ptr()
+    grad.data = torch.zeros(300, device=DEV)  # the step's buffer stays alive
+    assert torch.empty(300, device=DEV).data_ptr() != memory
+    keep = p.data
+    p.data = p.data.clone()
+    with pytest.raises(ValueError, match="moved"):
+        moe.adamw_step(opt, **HYPER)
+    p.data = keep
+    moe.adamw_step(opt, **HYPER)
+    assert int(opt.state[0]) == 1 and bool((p < 1).all())
+
+
+def test_adamw_blocks_before_the_first_tensor_belong_to_none():
+    # the tensor owns blocks 2 and 3; what lies before it in memory stays
+    buf, grad = torch.ones(1024, device=DEV), torch.ones(1024, device=DEV)
+    opt = moe.AdamW([buf], [grad])
+    opt._table[0, 0] += 512 * 4
+    opt._table[0, 2] += 512 * 4
+    opt._table[0, 3], opt._table[0, 4] = 512, 2
+    moe.adamw_step(opt, **HYPER)
+    assert bool((buf[:512] == 1).all()) and bool((buf[512:] < 1).all())
+    assert int(opt.m[:512].count_nonzero()) == 0 and bool((opt.m[512:] > 0).all())
 
 
 def test_adamw_values_that_are_not_numbers_are_not_hidden():

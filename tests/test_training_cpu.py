@@ -225,7 +225,14 @@ def test_adamw_refusals():
                 moe.MoEAdamW(2, 32, 1, 3, 8), moe.MoEAdamW(-1, 32, 1, 0, 8),
                 moe.MoEAdamW(2, 32, 1, 0, -1), moe.MoEAdamW(0, 32, 1, 0, 8)):
         assert call(bad) == 1
+    for eps in (1e-38, 1e-45, 1e31, inf, nan):  # subnormal, or too large
+        assert call(eps=eps) == 1, eps
     eight = moe.MoEAdamW(2, 8, 1, 0, 8)
+    for i in range(6):  # overlapping states, scales, table or step count
+        for j in range(i):
+            ptrs = _apart(6)
+            ptrs[i] = ptrs[j]
+            assert call(eight, ptrs=ptrs) == 1
     for i in (0, 1, 3, 5):
         for p in (None, P(8)):
             ptrs = _apart(6)
