@@ -21,10 +21,10 @@
 // multiply-add), so the states are exactly reproducible from the formulas.
 //
 // The step count lives on the device, so a captured step counts on when it is
-// replayed: a one-thread kernel adds one and writes the step's coefficients,
-// and the update kernel reads them. One warp per block: lane i owns elements
-// 8 i .. 8 i + 7, so all accesses are 8- to 16-byte vectors and the block's
-// maxima are warp reductions.
+// replayed. Each thread block reads it, works out the step's coefficients in
+// double precision and takes a ticket; the last one adds one to the count. One
+// warp per state block: lane i owns elements 8 i .. 8 i + 7, so all accesses are
+// 8- to 16-byte vectors and the block's maxima are warp reductions.
 #include <cuda_fp8.h>
 #include <float.h>
 #include <math.h>
@@ -40,8 +40,8 @@ constexpr int kAdamTable = 1024;  // tensors whose first blocks fit in shared me
 
 struct AdamState {  // moe_adamw_step's `state`, on the device
   int64_t step;
-  float size;  // lr / (1 - b1^t)
-  float inv_root;  // 1 / sqrt(1 - b2^t)
+  uint32_t tickets;  // thread blocks that have read the count; zero between steps
+  uint32_t unused;
 };
 
 struct AdamArgs {
@@ -50,19 +50,16 @@ struct AdamArgs {
   void* v;
   float* m_scale;
   float* v_scale;
-  const AdamState* state;
+  AdamState* state;
   int n_tensors;
   int64_t blocks;
+  double lr, beta1, beta2;
   float b1, omb1, b2, omb2, eps, keep;
 };
 
-__global__ void adamw_coef_kernel(AdamState* st, double lr, double b1, double b2) {
-  griddep_wait();
-  griddep_launch_dependents();
-  const int64_t t = st->step + 1;
-  st->step = t;
-  st->size = (float)(lr / (1.0 - pow(b1, (double)t)));
-  st->inv_root = (float)(1.0 / sqrt(1.0 - pow(b2, (double)t)));
+// 1 - b^t, kept out of the update kernel's registers.
+__device__ __noinline__ double correction(double b, int64_t t) {
+  return 1.0 - pow(b, (double)t);
 }
 
 template <typename T>
@@ -185,14 +182,31 @@ __device__ __forceinline__ void narrow8(const float* v, uint8_t* p, float* scale
 template <typename PT, typename GT, bool EIGHT>
 __global__ void __launch_bounds__(kAdamThreads) adamw_kernel(const AdamArgs a) {
   __shared__ int64_t s_first[kAdamTable];
+  __shared__ float s_size, s_inv_root;  // lr / (1 - b1^t), 1 / sqrt(1 - b2^t)
   griddep_wait();
   griddep_launch_dependents();
+  if (threadIdx.x == 0 || threadIdx.x == 32) {  // a warp each
+    const int64_t t = a.state->step + 1;
+    const bool first = threadIdx.x == 0;
+    const double c = correction(first ? a.beta1 : a.beta2, t);
+    if (first)
+      s_size = (float)(a.lr / c);
+    else
+      s_inv_root = (float)(1.0 / sqrt(c));
+  }
   const int n_t = a.n_tensors;
   const bool in_smem = n_t <= kAdamTable;
   if (in_smem)
     for (int i = threadIdx.x; i < n_t; i += kAdamThreads) s_first[i] = a.table[i].first_block;
   __syncthreads();
-  const float size = a.state->size, inv_root = a.state->inv_root;
+  const float size = s_size, inv_root = s_inv_root;
+  if (threadIdx.x == 0) {  // both of the block's reads of the count are done
+    __threadfence();
+    if (atomicAdd(&a.state->tickets, 1u) == gridDim.x - 1) {
+      a.state->tickets = 0;
+      a.state->step += 1;
+    }
+  }
   const int lane = threadIdx.x & 31;
   const int64_t warps = (int64_t)gridDim.x * (kAdamThreads / 32);
   for (int64_t b = (int64_t)blockIdx.x * (kAdamThreads / 32) + (threadIdx.x >> 5); b < a.blocks;
@@ -251,6 +265,7 @@ cudaError_t run_adamw(const AdamArgs& a, bool eight, cudaStream_t st) {
   int64_t grid = (a.blocks + kAdamThreads / 32 - 1) / (kAdamThreads / 32);
   const int64_t cap = (int64_t)num_sms() * 16;
   if (grid > cap) grid = cap;
+  if (grid < 1) grid = 1;  // no tensors: the step still counts
   return launch_pdl(eight ? adamw_kernel<PT, GT, true> : adamw_kernel<PT, GT, false>,
                     dim3((unsigned)grid), dim3(kAdamThreads), 0, st, a);
 }
@@ -297,19 +312,17 @@ extern "C" moe_status_t moe_adamw_step(const moe_adamw_t* opt, const moe_adamw_p
                          {state, sizeof(AdamState), true}};
   if (!disjoint(spans)) return MOE_ERR_INVALID_ARG;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  AdamState* s = static_cast<AdamState*>(state);
-  cudaError_t e =
-      launch_pdl(adamw_coef_kernel, dim3(1), dim3(1), 0, st, s, h.lr, h.beta1, h.beta2);
-  if (e != cudaSuccess) return MOE_ERR_CUDA;
-  if (!any) return MOE_OK;
   AdamArgs a;
   a.table = table;
   a.m = m;
   a.v = v;
   a.m_scale = m_scale;
   a.v_scale = v_scale;
-  a.state = s;
-  a.n_tensors = o.n_tensors;
+  a.state = static_cast<AdamState*>(state);
+  a.n_tensors = any ? o.n_tensors : 0;
+  a.lr = h.lr;
+  a.beta1 = h.beta1;
+  a.beta2 = h.beta2;
   a.blocks = o.total_blocks;
   a.b1 = (float)h.beta1;
   a.omb1 = (float)(1.0 - h.beta1);
@@ -318,6 +331,7 @@ extern "C" moe_status_t moe_adamw_step(const moe_adamw_t* opt, const moe_adamw_p
   a.eps = (float)h.eps;
   a.keep = (float)(1.0 - h.lr * h.weight_decay);
   const bool pb = o.param_dtype == MOE_BF16, gb = o.grad_dtype == MOE_BF16;
+  cudaError_t e;
   if (pb)
     e = gb ? run_adamw<__nv_bfloat16, __nv_bfloat16>(a, eight, st)
            : run_adamw<__nv_bfloat16, float>(a, eight, st);

@@ -652,6 +652,15 @@ def test_adamw_refuses_weights_that_moved():
     assert int(opt.state[0]) == 1 and bool((p < 1).all())
 
 
+@pytest.mark.parametrize("bits", [32, 8])
+def test_adamw_step_of_no_elements_counts(bits):
+    none = torch.empty(0, device=DEV)
+    opt = moe.AdamW([none], [none.clone()], state_bits=bits)
+    for _ in range(3):
+        moe.adamw_step(opt, **HYPER)
+    assert opt.state.tolist() == [3, 0]
+
+
 def test_adamw_blocks_before_the_first_tensor_belong_to_none():
     # the tensor owns blocks 2 and 3; what lies before it in memory stays
     buf, grad = torch.ones(1024, device=DEV), torch.ones(1024, device=DEV)
