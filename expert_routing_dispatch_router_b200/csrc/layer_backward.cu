@@ -17,6 +17,40 @@
 namespace moe {
 namespace {
 
+// Two floats in one 64-bit register, and the operations on both at once: each
+// half is rounded as the single operation would, at half the instructions.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ ulonglong2 load_pairs(const float* p) {
+  const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
+  return make_ulonglong2((uint64_t)u.y << 32 | u.x, (uint64_t)u.w << 32 | u.z);
+}
+
+// Element `at` of row `row`; rows are shorter than 2^32 elements, so one wide
+// multiply has the offset.
+template <typename T>
+__device__ __forceinline__ const T* in_row(const T* p, int row, uint32_t d, int64_t col) {
+  return p + col + (uint64_t)(uint32_t)row * d;
+}
+
 // 16 bytes of activations along d.
 template <typename AT>
 struct Chunk;
@@ -31,6 +65,7 @@ struct Chunk<__nv_bfloat16> {
     const uint32_t w = i < 2 ? u.x : (i < 4 ? u.y : (i < 6 ? u.z : u.w));
     return (i & 1) ? __uint_as_float(w & 0xffff0000u) : __uint_as_float(w << 16);
   }
+  __device__ uint64_t pair(int i) const { return pack2(get(2 * i), get(2 * i + 1)); }
   __device__ static void store(__nv_bfloat16* p, const float* v) {
     uint32_t w[4];
 #pragma unroll
@@ -51,6 +86,7 @@ struct Chunk<float> {
   __device__ float get(int i) const {
     return i == 0 ? f.x : (i == 1 ? f.y : (i == 2 ? f.z : f.w));
   }
+  __device__ uint64_t pair(int i) const { return pack2(get(2 * i), get(2 * i + 1)); }
   __device__ static void store(float* p, const float* v) {
     *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
   }
@@ -275,30 +311,31 @@ __global__ void __launch_bounds__(kDwThreads)
     }
     __syncthreads();
     if (col < d) {
-      float acc[V];
+      uint64_t acc[V / 2];
 #pragma unroll
-      for (int i = 0; i < V; ++i) acc[i] = 0.f;
+      for (int i = 0; i < V / 2; ++i) acc[i] = 0;
       for (int r = 0; r < n; r += 8) {
         Chunk<AT> xv[8];
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
           if (r + q < n)
-            xv[q].load(x + (int64_t)s_tok[r + q] * d + col);
+            xv[q].load(in_row(x, s_tok[r + q], (uint32_t)d, col));
           else
             xv[q].zero();
         }
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
           if (r + q >= n) continue;
-          const float w = s_dl[r + q];
+          const uint64_t w = pack2(s_dl[r + q], s_dl[r + q]);
 #pragma unroll
-          for (int i = 0; i < V; ++i) acc[i] = fmaf(w, xv[q].get(i), acc[i]);
+          for (int i = 0; i < V / 2; ++i) acc[i] = fma2(w, xv[q].pair(i), acc[i]);
         }
       }
 #pragma unroll
-      for (int i = 0; i < V; i += 4)
-        store4(part + (int64_t)c * d + col + i,
-               make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]));
+      for (int i = 0; i < V / 2; i += 2) {
+        const float2 lo = unpack2(acc[i]), hi = unpack2(acc[i + 1]);
+        store4(part + (int64_t)c * d + col + 2 * i, make_float4(lo.x, lo.y, hi.x, hi.y));
+      }
     }
   }
 }
@@ -360,23 +397,23 @@ __global__ void __launch_bounds__(128)
     g.zero();
   __syncthreads();
   if (col >= d) return;
-  float acc[V];
+  uint64_t acc[V / 2], r[V / 2];
 #pragma unroll
-  for (int i = 0; i < V; ++i) acc[i] = 0.f;
+  for (int i = 0; i < V / 2; ++i) acc[i] = r[i] = 0;
   for (int j0 = 0; j0 < k; j0 += kSlotGroup) {
     Chunk<AT> v[kSlotGroup];
 #pragma unroll
     for (int q = 0; q < kSlotGroup; ++q) {
       const int j = j0 + q;
       if (j < k && s_row[j] >= 0)
-        v[q].load(dx_perm + (int64_t)s_row[j] * d + col);
+        v[q].load(in_row(dx_perm, s_row[j], (uint32_t)d, col));
       else
         v[q].zero();
     }
 #pragma unroll
     for (int q = 0; q < kSlotGroup; ++q)
 #pragma unroll
-      for (int i = 0; i < V; ++i) acc[i] += v[q].get(i);
+      for (int i = 0; i < V / 2; ++i) acc[i] = add2(acc[i], v[q].pair(i));
   }
   float zero = 0.f;
   bool any_zero = false;
@@ -386,35 +423,35 @@ __global__ void __launch_bounds__(128)
   }
   if (any_zero) {  // a token without zero experts does not see dout here
 #pragma unroll
-    for (int i = 0; i < V; ++i) acc[i] = fmaf(zero, g.get(i), acc[i]);
+    for (int i = 0; i < V / 2; ++i) acc[i] = fma2(pack2(zero, zero), g.pair(i), acc[i]);
   }
-  float r[V];
-#pragma unroll
-  for (int i = 0; i < V; ++i) r[i] = 0.f;
   for (int j0 = 0; j0 < k; j0 += 4) {
-    float4 w[4][V / 4];
+    ulonglong2 w[4][V / 4];
 #pragma unroll
     for (int q = 0; q < 4; ++q)
 #pragma unroll
       for (int i = 0; i < V / 4; ++i)
         w[q][i] = j0 + q < k && s_e[j0 + q] >= 0
-                      ? load4(w_router + (int64_t)s_e[j0 + q] * d + col + 4 * i)
-                      : make_float4(0.f, 0.f, 0.f, 0.f);
+                      ? load_pairs(in_row(w_router, s_e[j0 + q], (uint32_t)d, col) + 4 * i)
+                      : make_ulonglong2(0, 0);
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const float dl = j0 + q < k ? s_dl[j0 + q] : 0.f;
 #pragma unroll
       for (int i = 0; i < V / 4; ++i) {
-        r[4 * i] = fmaf(dl, w[q][i].x, r[4 * i]);
-        r[4 * i + 1] = fmaf(dl, w[q][i].y, r[4 * i + 1]);
-        r[4 * i + 2] = fmaf(dl, w[q][i].z, r[4 * i + 2]);
-        r[4 * i + 3] = fmaf(dl, w[q][i].w, r[4 * i + 3]);
+        r[2 * i] = fma2(pack2(dl, dl), w[q][i].x, r[2 * i]);
+        r[2 * i + 1] = fma2(pack2(dl, dl), w[q][i].y, r[2 * i + 1]);
       }
     }
   }
+  float out[V];
 #pragma unroll
-  for (int i = 0; i < V; ++i) acc[i] += r[i];
-  Chunk<AT>::store(dx + t * d + col, acc);
+  for (int i = 0; i < V / 2; ++i) {
+    const float2 o = unpack2(add2(acc[i], r[i]));
+    out[2 * i] = o.x;
+    out[2 * i + 1] = o.y;
+  }
+  Chunk<AT>::store(dx + t * d + col, out);
 }
 
 template <typename T>
