@@ -708,8 +708,8 @@ class AdamW:
     """The states of an AdamW optimizer over fixed weights and gradient buffers
     (step it with adamw_step). The tensors are kept alive and updated in place;
     a step reads whatever the gradient buffers hold then. They stay in the
-    memory they had at construction: a step refuses a weight that has moved since
-    (a replayed step cannot).
+    memory they had at construction: a step refuses a weight, master or state
+    that has moved since (a replayed step cannot).
 
     params: float32 or bfloat16 CUDA tensors, one type for all; grads: tensors
     of the same sizes, one type for all. master: float32 copies of bfloat16
@@ -746,9 +746,9 @@ class AdamW:
         self._refuse_overlaps([t for t in params + master if t is not None], grads)
         self.params, self.grads, self.master = params, grads, master
         self.state_bits = state_bits
+        self._mastered = any(w is not None for w in master)
         dev = params[0].device
         self._memory = [t.detach() for t in params + grads + master if t is not None]
-        self._addresses = [p.data_ptr() for p in params]
         rows, at = [], 0
         for p, g, w in zip(params, grads, master):
             rows.append([p.data_ptr(), 0 if w is None else w.data_ptr(), g.data_ptr(),
@@ -767,6 +767,15 @@ class AdamW:
             self.m, self.v = ((torch.zeros(n, dtype=torch.float8_e4m3fn, device=dev),
                                torch.zeros(at, device=dev)) for _ in range(2))
         self.state = torch.zeros(2, dtype=torch.int64, device=dev)  # step count, scratch
+        self._memory += [t.detach() for t in (*((self.m, self.v) if state_bits == 32 else
+                                                (*self.m, *self.v)), self.state)]
+        self._addresses = self._fixed_addresses()
+
+    def _fixed_addresses(self):
+        """Where everything that a step writes lies now."""
+        states = (self.m, self.v) if self.state_bits == 32 else (*self.m, *self.v)
+        masters = [w for w in self.master if w is not None] if self._mastered else ()
+        return list(map(_DATA_PTR, [*self.params, *masters, *states, self.state]))
 
     @staticmethod
     def _refuse_overlaps(written, read):
@@ -802,8 +811,8 @@ def adamw_step(opt: AdamW, lr: float, beta1: float = 0.9, beta2: float = 0.999,
     hyper = MoEAdamWParams(lr, beta1, beta2, eps, weight_decay)
     m, ms = opt.m if opt.state_bits == 8 else (opt.m, None)
     v, vs = opt.v if opt.state_bits == 8 else (opt.v, None)
-    if list(map(_DATA_PTR, opt.params)) != opt._addresses:
-        raise ValueError("a weight has moved to other memory")
+    if opt._fixed_addresses() != opt._addresses:
+        raise ValueError("a weight, master or state has moved to other memory")
     _on_current_device(opt._table)
     st = lib().moe_adamw_step(ctypes.byref(opt._c), ctypes.byref(hyper), _ptr(opt._table),
                               _ptr(m), _ptr(ms), _ptr(v), _ptr(vs), _ptr(opt.state),

@@ -653,6 +653,29 @@ def test_adamw_refuses_weights_that_moved():
 
 
 @pytest.mark.parametrize("bits", [32, 8])
+def test_adamw_refuses_masters_and_states_that_moved(bits):
+    p, grad = torch.ones(300, dtype=BF, device=DEV), torch.ones(300, dtype=BF, device=DEV)
+    opt = moe.AdamW([p], [grad], state_bits=bits, master=[p.float()])
+    parts = [opt.master[0], opt.state, *((opt.m, opt.v) if bits == 32 else (*opt.m, *opt.v))]
+    for t in parts:  # as a loaded checkpoint would be put in their place
+        keep = t.data
+        t.data = keep.clone()
+        with pytest.raises(ValueError, match="moved"):
+            moe.adamw_step(opt, **HYPER)
+        t.data = keep
+    for name in ("m", "v"):  # a state of another size would be written past its end
+        keep = getattr(opt, name)
+        setattr(opt, name, torch.zeros(256, device=DEV) if bits == 32
+                else tuple(t.clone() for t in keep))
+        with pytest.raises(ValueError, match="moved"):
+            moe.adamw_step(opt, **HYPER)
+        setattr(opt, name, keep)
+    assert int(opt.state[0]) == 0 and bool((p == 1).all())
+    moe.adamw_step(opt, **HYPER)
+    assert int(opt.state[0]) == 1 and bool((opt.master[0] < 1).all())
+
+
+@pytest.mark.parametrize("bits", [32, 8])
 def test_adamw_step_of_no_elements_counts(bits):
     none = torch.empty(0, device=DEV)
     opt = moe.AdamW([none], [none.clone()], state_bits=bits)

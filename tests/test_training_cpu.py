@@ -316,3 +316,42 @@ def test_tensors_of_another_device_are_refused(monkeypatch):
     moe._on_current_device(here, None, here)
     with pytest.raises(ValueError, match="cuda:0"):
         moe._on_current_device(here, there)
+
+
+# ------------------------------------- the optimizer's buffers, on the host --
+@pytest.fixture
+def host_adamw(monkeypatch):
+    """The binding over host tensors, with a step that only notes its call (the
+    device checks are relaxed for these tests only)."""
+    import types
+    real, calls = moe._need, []
+    monkeypatch.setattr(moe, "_need", lambda t, n, dt, shape=None, on_device=True:
+                        real(t, n, dt, shape, on_device=False))
+    monkeypatch.setattr(moe, "_on_current_device", lambda *tensors: None)
+    monkeypatch.setattr(moe, "lib", lambda: types.SimpleNamespace(
+        moe_adamw_step=lambda *a: calls.append(a) or 0))
+    return types.SimpleNamespace(calls=calls, stream=types.SimpleNamespace(cuda_stream=0))
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_adamw_refuses_buffers_that_moved(host_adamw, bits):
+    bf = torch.bfloat16
+    p, grad = torch.ones(300, dtype=bf), torch.ones(300, dtype=bf)
+    opt = moe.AdamW([p], [grad], state_bits=bits, master=[p.float()])
+    step = lambda: moe.adamw_step(opt, lr=1e-3, stream=host_adamw.stream)  # noqa: E731
+    step()
+    for t in (p, opt.master[0], opt.state, *((opt.m, opt.v) if bits == 32
+                                             else (*opt.m, *opt.v))):
+        keep = t.data
+        t.data = keep.clone()
+        with pytest.raises(ValueError, match="moved"):
+            step()
+        t.data = keep
+    for name in ("m", "v"):  # a state put in another's place, of any size
+        keep = getattr(opt, name)
+        setattr(opt, name, torch.zeros(256) if bits == 32 else tuple(t.clone() for t in keep))
+        with pytest.raises(ValueError, match="moved"):
+            step()
+        setattr(opt, name, keep)
+    step()
+    assert len(host_adamw.calls) == 2
