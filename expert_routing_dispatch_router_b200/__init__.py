@@ -704,12 +704,25 @@ ADAMW_BLOCK = 256  # elements per state block
 _DATA_PTR = torch.Tensor.data_ptr
 
 
+def _capturing(stream=None) -> bool:
+    """Whether the call's stream is being captured into a graph."""
+    if stream is None:
+        return torch.cuda.is_current_stream_capturing()
+    with torch.cuda.stream(stream):
+        return torch.cuda.is_current_stream_capturing()
+
+
 class AdamW:
     """The states of an AdamW optimizer over fixed weights and gradient buffers
-    (step it with adamw_step). The tensors are kept alive and updated in place;
-    a step reads whatever the gradient buffers hold then. They stay in the
-    memory they had at construction: a step refuses a weight, master or state
-    that has moved since (a replayed step cannot).
+    (step it with adamw_step). The tensors are kept alive and updated in place.
+    Weights, masters and states stay in the memory they had at construction: a
+    step refuses one that has moved since (a replayed step cannot).
+
+    A step reads what the tensors of ``grads`` hold then. One that lies in other
+    memory than at the step before (its ``data`` assigned, or another tensor put
+    in its place) is checked anew and taken up, for which the step waits for the
+    device; a step under capture refuses it. A replayed step reads the memory of
+    its capture, which is kept alive.
 
     params: float32 or bfloat16 CUDA tensors, one type for all; grads: tensors
     of the same sizes, one type for all. master: float32 copies of bfloat16
@@ -731,34 +744,21 @@ class AdamW:
         for what, dt in (("params", pdt), ("grads", gdt)):
             if dt not in _DTYPE_CODE:
                 raise ValueError(f"{what}: dtype {dt}, expected float32 or bfloat16")
-        for i, (p, g, w) in enumerate(zip(params, grads, master)):
-            _need(p, f"params[{i}]", pdt)
-            _need(g, f"grads[{i}]", gdt, p.shape)
-            if w is not None:
-                if pdt != torch.bfloat16:
-                    raise ValueError("master: only for bfloat16 weights")
-                _need(w, f"master[{i}]", torch.float32, p.shape)
-            for t in (p, g) if w is None else (p, g, w):
-                if t.device != params[0].device:
-                    raise ValueError("all tensors must be on one device")
-                if t.data_ptr() % 16:
-                    raise ValueError("every tensor must be 16-byte aligned")
-        self._refuse_overlaps([t for t in params + master if t is not None], grads)
+        if any(w is not None for w in master) and pdt != torch.bfloat16:
+            raise ValueError("master: only for bfloat16 weights")
+        self._check_tensors(params, grads, master, pdt, gdt)
         self.params, self.grads, self.master = params, grads, master
         self.state_bits = state_bits
         self._mastered = any(w is not None for w in master)
         dev = params[0].device
-        self._memory = [t.detach() for t in params + grads + master if t is not None]
-        rows, at = [], 0
-        for p, g, w in zip(params, grads, master):
-            rows.append([p.data_ptr(), 0 if w is None else w.data_ptr(), g.data_ptr(),
-                         p.numel(), at, 0])
-            at += -(-p.numel() // ADAMW_BLOCK)
-        # a tensor without elements has no block: it is left out of the table
-        rows = [r for r in rows if r[3] > 0]
+        self._memory = [t.detach() for t in params + master if t is not None]
+        sizes = [p.numel() for p in params]
+        at = sum(-(-n // ADAMW_BLOCK) for n in sizes)
         self.total_blocks = at
-        self._c = MoEAdamW(len(rows), state_bits, _DTYPE_CODE[pdt], _DTYPE_CODE[gdt], at)
-        self._table = torch.tensor(rows, dtype=torch.int64).reshape(-1, 6).to(dev)
+        self._c = MoEAdamW(sum(n > 0 for n in sizes), state_bits, _DTYPE_CODE[pdt],
+                           _DTYPE_CODE[gdt], at)
+        self._kept = []  # what captured steps read, once the gradients have moved
+        self._captured = False
         n = at * ADAMW_BLOCK
         if state_bits == 32:
             self.m = torch.zeros(n, device=dev)
@@ -769,13 +769,65 @@ class AdamW:
         self.state = torch.zeros(2, dtype=torch.int64, device=dev)  # step count, scratch
         self._memory += [t.detach() for t in (*((self.m, self.v) if state_bits == 32 else
                                                 (*self.m, *self.v)), self.state)]
-        self._addresses = self._fixed_addresses()
+        self._take_gradients()
+        self._addresses = self._lie_at()
 
-    def _fixed_addresses(self):
-        """Where everything that a step writes lies now."""
+    @classmethod
+    def _check_tensors(cls, params, grads, master, pdt, gdt):
+        for i, (p, g, w) in enumerate(zip(params, grads, master)):
+            _need(p, f"params[{i}]", pdt)
+            _need(g, f"grads[{i}]", gdt, p.shape)
+            if w is not None:
+                _need(w, f"master[{i}]", torch.float32, p.shape)
+            for t in (p, g) if w is None else (p, g, w):
+                if t.device != params[0].device:
+                    raise ValueError("all tensors must be on one device")
+                if t.data_ptr() % 16:
+                    raise ValueError("every tensor must be 16-byte aligned")
+        cls._refuse_overlaps([t for t in params + master if t is not None], grads)
+
+    def _take_gradients(self):
+        """The table of all tensors, with the gradients where they lie now."""
+        rows, at = [], 0
+        for p, g, w in zip(self.params, self.grads, self.master):
+            rows.append([p.data_ptr(), 0 if w is None else w.data_ptr(), g.data_ptr(),
+                         p.numel(), at, 0])
+            at += -(-p.numel() // ADAMW_BLOCK)
+        # a tensor without elements has no block: it is left out of the table
+        rows = [r for r in rows if r[3] > 0]
+        self._table = torch.tensor(rows, dtype=torch.int64).reshape(-1, 6).to(
+            self.params[0].device)
+        self._grad_memory = [g.detach() for g in self.grads]
+        (m, ms), (v, vs) = ((self.m, None), (self.v, None)) if self.state_bits == 32 else (
+            self.m, self.v)
+        self._pointers = tuple(map(_ptr, (self._table, m, ms, v, vs, self.state)))
+
+    def _moved(self, now, capturing):
+        """Something lies in other memory (`now`) than at the last step: only
+        gradients may."""
+        n = len(self.grads)
+        if now[n:] != self._addresses[len(self._grad_memory):]:
+            raise ValueError("a weight, master or state has moved to other memory")
+        if capturing:
+            raise ValueError("a gradient has moved to other memory, which a step under "
+                             "capture cannot follow")
+        if n != len(self.params):
+            raise ValueError("one gradient per weight")
+        self._check_tensors(self.params, self.grads, self.master, self.params[0].dtype,
+                            self._grad_memory[0].dtype)
+        if self._captured:
+            self._kept.append((self._table, self._grad_memory))
+            self._captured = False
+        elif self._table.is_cuda:  # steps in flight still read the table
+            torch.cuda.synchronize(self._table.device)
+        self._take_gradients()
+        self._addresses = now
+
+    def _lie_at(self):
+        """Where the gradients and everything that a step writes lie now."""
         states = (self.m, self.v) if self.state_bits == 32 else (*self.m, *self.v)
         masters = [w for w in self.master if w is not None] if self._mastered else ()
-        return list(map(_DATA_PTR, [*self.params, *masters, *states, self.state]))
+        return list(map(_DATA_PTR, [*self.grads, *self.params, *masters, *states, self.state]))
 
     @staticmethod
     def _refuse_overlaps(written, read):
@@ -804,18 +856,17 @@ class AdamW:
 
 def adamw_step(opt: AdamW, lr: float, beta1: float = 0.9, beta2: float = 0.999,
                eps: float = 1e-8, weight_decay: float = 0.0, stream=None):
-    """One AdamW step of every tensor of `opt`, in place, from what its gradient
-    buffers hold. The step count lives on the device, so a step captured in a
+    """One AdamW step of every tensor of `opt`, in place, from what its gradients
+    hold. The step count lives on the device, so a step captured in a
     CUDA graph counts on when it is replayed (its lr and betas are those of the
     capture)."""
     hyper = MoEAdamWParams(lr, beta1, beta2, eps, weight_decay)
-    m, ms = opt.m if opt.state_bits == 8 else (opt.m, None)
-    v, vs = opt.v if opt.state_bits == 8 else (opt.v, None)
-    if opt._fixed_addresses() != opt._addresses:
-        raise ValueError("a weight, master or state has moved to other memory")
+    capturing, now = _capturing(stream), opt._lie_at()
+    if now != opt._addresses:
+        opt._moved(now, capturing)
+    if capturing:
+        opt._captured = True
     _on_current_device(opt._table)
-    st = lib().moe_adamw_step(ctypes.byref(opt._c), ctypes.byref(hyper), _ptr(opt._table),
-                              _ptr(m), _ptr(ms), _ptr(v), _ptr(vs), _ptr(opt.state),
-                              _stream(stream))
+    st = lib().moe_adamw_step(opt._c, ctypes.byref(hyper), *opt._pointers, _stream(stream))
     _check("moe_adamw_step", st)
     return opt

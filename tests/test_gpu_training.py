@@ -675,6 +675,37 @@ def test_adamw_refuses_masters_and_states_that_moved(bits):
     assert int(opt.state[0]) == 1 and bool((opt.master[0] < 1).all())
 
 
+def test_adamw_steps_from_gradients_that_moved():
+    # first gradients of one sign, then others in new memory of the other sign:
+    # every step follows what the gradients hold; a replay reads its capture's
+    # five quotients within 2 units of 2^-23, times lr and rounded: 5 * 2^-22
+    at = lambda v: bool(((p - v).abs() <= 5 * 2.0 ** -22).all())  # noqa: E731
+    p = torch.zeros(700, device=DEV)
+    grad = torch.ones(700, device=DEV)
+    opt = moe.AdamW([p], [grad])
+    h = dict(lr=0.5, beta1=0.0, beta2=0.0)  # a step moves every weight by lr
+    moe.adamw_step(opt, **h)
+    assert at(-0.5)
+    grad.data = torch.full((700,), -3.0, device=DEV)
+    moe.adamw_step(opt, **h)
+    assert at(0.0)
+    opt.grads[0] = torch.full((700,), 2.0, device=DEV)
+    moe.adamw_step(opt, **h)
+    assert at(-0.5)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        moe.adamw_step(opt, **h)
+    kept = opt.grads[0]
+    opt.grads[0] = torch.full((700,), -1.0, device=DEV)
+    moe.adamw_step(opt, **h)
+    assert at(0.0)
+    kept.fill_(5.0)
+    del kept
+    graph.replay()
+    assert at(-0.5) and int(opt.state[0]) == 5
+
+
 @pytest.mark.parametrize("bits", [32, 8])
 def test_adamw_step_of_no_elements_counts(bits):
     none = torch.empty(0, device=DEV)

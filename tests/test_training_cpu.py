@@ -328,9 +328,12 @@ def host_adamw(monkeypatch):
     monkeypatch.setattr(moe, "_need", lambda t, n, dt, shape=None, on_device=True:
                         real(t, n, dt, shape, on_device=False))
     monkeypatch.setattr(moe, "_on_current_device", lambda *tensors: None)
+    state = types.SimpleNamespace(capturing=False)
+    monkeypatch.setattr(moe, "_capturing", lambda stream=None: state.capturing, raising=False)
     monkeypatch.setattr(moe, "lib", lambda: types.SimpleNamespace(
         moe_adamw_step=lambda *a: calls.append(a) or 0))
-    return types.SimpleNamespace(calls=calls, stream=types.SimpleNamespace(cuda_stream=0))
+    state.calls, state.stream = calls, types.SimpleNamespace(cuda_stream=0)
+    return state
 
 
 @pytest.mark.parametrize("bits", [32, 8])
@@ -355,3 +358,42 @@ def test_adamw_refuses_buffers_that_moved(host_adamw, bits):
         setattr(opt, name, keep)
     step()
     assert len(host_adamw.calls) == 2
+
+
+def test_adamw_reads_gradients_where_they_lie(host_adamw):
+    params = [torch.ones(300), torch.ones(0), torch.ones(5)]
+    grads = [torch.ones(300), torch.ones(0), torch.ones(5)]
+    opt = moe.AdamW(params, grads)
+    step = lambda: moe.adamw_step(opt, lr=1e-3, stream=host_adamw.stream)  # noqa: E731
+    seen = lambda: opt._table[:, 2].tolist()  # noqa: E731
+    step()
+    first, table = seen(), opt._table
+    grads[0].data = torch.zeros(300)
+    step()
+    assert seen() == [grads[0].data_ptr(), grads[2].data_ptr()] != first
+    other = torch.zeros(5)
+    opt.grads[2] = other  # another tensor in its place
+    step()
+    assert seen() == [grads[0].data_ptr(), other.data_ptr()]
+    assert opt._table[:, [0, 1, 3, 4, 5]].equal(table[:, [0, 1, 3, 4, 5]])
+    # what construction refuses is refused here too, and the step is not made
+    for bad, match in ((torch.zeros(6), "shape"), (torch.zeros(5, dtype=torch.bfloat16), "dtype"),
+                       (torch.zeros(10)[::2], "contiguous"), (torch.zeros(6)[1:], "aligned"),
+                       (params[0][:5], "overlaps")):
+        opt.grads[2] = bad
+        with pytest.raises(ValueError, match=match):
+            step()
+    opt.grads[2] = other
+    step()
+    assert len(host_adamw.calls) == 4
+    # a captured step's table and gradients stay; a step under capture refuses
+    host_adamw.capturing = True
+    step()
+    captured = opt._table
+    opt.grads[2] = torch.zeros(5)
+    with pytest.raises(ValueError, match="capture"):
+        step()
+    host_adamw.capturing = False
+    step()
+    assert opt._kept[0][0] is captured and opt._kept[0][1][2].data_ptr() == other.data_ptr()
+    assert opt._table is not captured and len(opt._kept) == 1
