@@ -222,6 +222,33 @@ def _ws(ws: torch.Tensor):
     return ctypes.c_void_p(ws.data_ptr()), ws.numel() * ws.element_size()
 
 
+def _new(shape, dtype, device, stream):
+    """A new output of a call on `stream`. torch hands out memory stream by
+    stream, so it is taken from the call's own: nobody else still uses it when
+    the call writes it, and it is not handed out again before the call is done,
+    even if the caller drops it at once. The current stream, where the caller
+    goes on with it, is noted as a second user."""
+    if stream is None or device.type != "cuda":
+        return torch.empty(shape, dtype=dtype, device=device)
+    current = torch.cuda.current_stream(device)
+    if stream.cuda_stream == current.cuda_stream:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream, device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(current)
+    return t
+
+
+def _out(t, name, dtype, shape, device, stream):
+    """An output the caller gave (checked), or a new one."""
+    if t is None:
+        return _new(shape, dtype, device, stream)
+    _need(t, name, dtype, shape)
+    return t
+
+
 def workspace_size(shape: LayerShape) -> int:
     return int(lib().moe_workspace_size(ctypes.byref(shape.c())))
 
@@ -245,8 +272,8 @@ def route(shape: LayerShape, x, w_router, bias, ws, logits=None, flags=None,
     _need(x, "x", shape.act_dtype, (T, shape.d))
     _need(w_router, "w_router", torch.float32, (E, shape.d))
     _need(bias, "bias", torch.float32, (E,))
-    idx = torch.empty(T, k, dtype=torch.int32, device=x.device)
-    gate = torch.empty(T, k, dtype=torch.float32, device=x.device)
+    idx = _new((T, k), torch.int32, x.device, stream)
+    gate = _new((T, k), torch.float32, x.device, stream)
     if logits is not None:
         _need(logits, "logits", torch.float32, (T, E))
     if flags is not None:
@@ -286,12 +313,12 @@ def dispatch(shape: LayerShape, x, topk_idx, ws, stream=None):
     T, k = shape.T, shape.top_k
     _need(x, "x", shape.act_dtype, (T, shape.d))
     _need(topk_idx, "topk_idx", torch.int32, (T, k))
-    dev = x.device
-    counts = torch.empty(shape.E, dtype=torch.int32, device=dev)
-    offsets = torch.empty(shape.n_routed + 1, dtype=torch.int32, device=dev)
-    row_token = torch.empty(T * k, dtype=torch.int32, device=dev)
-    slot_row = torch.empty(T * k, dtype=torch.int32, device=dev)
-    x_perm = torch.empty(T * k, shape.d, dtype=shape.act_dtype, device=dev)
+    dev, i32 = x.device, torch.int32
+    counts = _new((shape.E,), i32, dev, stream)
+    offsets = _new((shape.n_routed + 1,), i32, dev, stream)
+    row_token = _new((T * k,), i32, dev, stream)
+    slot_row = _new((T * k,), i32, dev, stream)
+    x_perm = _new((T * k, shape.d), shape.act_dtype, dev, stream)
     st = lib().moe_dispatch(ctypes.byref(shape.c()), _ptr(x), _ptr(topk_idx),
                             _ptr(counts), _ptr(offsets), _ptr(row_token),
                             _ptr(slot_row), _ptr(x_perm), *_ws(ws),
@@ -309,9 +336,7 @@ def expert_ffn(shape: LayerShape, x_perm, offsets, w_gate, w_up, w_down, ws,
     for name, w, shp in (("w_gate", w_gate, (N, F, d)), ("w_up", w_up, (N, F, d)),
                          ("w_down", w_down, (N, d, F))):
         _need(w, name, shape.act_dtype, shp)
-    if y_perm is None:
-        y_perm = torch.empty(T * k, d, dtype=shape.act_dtype, device=x_perm.device)
-    _need(y_perm, "y_perm", shape.act_dtype, (T * k, d))
+    y_perm = _out(y_perm, "y_perm", shape.act_dtype, (T * k, d), x_perm.device, stream)
     st = lib().moe_expert_ffn(ctypes.byref(shape.c()), _ptr(x_perm), _ptr(offsets),
                               _ptr(w_gate), _ptr(w_up), _ptr(w_down), _ptr(y_perm),
                               *_ws(ws), _stream(stream))
@@ -327,9 +352,7 @@ def combine(shape: LayerShape, x, y_perm, topk_idx, topk_gate, slot_row, out=Non
     _need(topk_idx, "topk_idx", torch.int32, (T, k))
     _need(topk_gate, "topk_gate", torch.float32, (T, k))
     _need(slot_row, "slot_row", torch.int32, (T * k,))
-    if out is None:
-        out = torch.empty(T, d, dtype=shape.act_dtype, device=x.device)
-    _need(out, "out", shape.act_dtype, (T, d))
+    out = _out(out, "out", shape.act_dtype, (T, d), x.device, stream)
     st = lib().moe_combine(ctypes.byref(shape.c()), _ptr(x), _ptr(y_perm),
                            _ptr(topk_idx), _ptr(topk_gate), _ptr(slot_row), _ptr(out),
                            _stream(stream))
@@ -362,9 +385,8 @@ def ep_plan(shape: LayerShape, rank: int, world: int, counts_all, stream=None):
     N, E = shape.n_routed, shape.E
     _need(counts_all, "counts_all", torch.int32, (world, E))
     dev = counts_all.device
-    dest_row = torch.empty(N, dtype=torch.int32, device=dev)
-    recv_offsets = torch.empty(ep_local_experts(shape, rank, world) + 1, dtype=torch.int32,
-                               device=dev)
+    dest_row = _new((N,), torch.int32, dev, stream)
+    recv_offsets = _new((ep_local_experts(shape, rank, world) + 1,), torch.int32, dev, stream)
     st = lib().moe_ep_plan(ctypes.byref(shape.c()), rank, world, _ptr(counts_all),
                            _ptr(dest_row), _ptr(recv_offsets), _stream(stream))
     _check("moe_ep_plan", st)
@@ -421,9 +443,7 @@ def layer_forward(shape: LayerShape, x, w_router, bias, w_gate, w_up, w_down, ws
         for name, w, shp in (("w_gate", w_gate, (N, F, d)), ("w_up", w_up, (N, F, d)),
                              ("w_down", w_down, (N, d, F))):
             _need(w, name, shape.act_dtype, shp)
-    if out is None:
-        out = torch.empty(T, d, dtype=shape.act_dtype, device=x.device)
-    _need(out, "out", shape.act_dtype, (T, d))
+    out = _out(out, "out", shape.act_dtype, (T, d), x.device, stream)
     if counts is not None:
         _need(counts, "counts", torch.int32, (E,))
     st = lib().moe_layer_forward(ctypes.byref(shape.c()), _ptr(x), _ptr(w_router),
@@ -507,14 +527,6 @@ def alloc_grouped_workspace(shape: GroupedShape, device="cuda") -> torch.Tensor:
     return torch.zeros(n, dtype=torch.uint8, device=device)
 
 
-def _out(t, name, dtype, shape, device):
-    """An output the caller gave (checked), or a new one."""
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    _need(t, name, dtype, shape)
-    return t
-
-
 def grouped_matmul(shape: GroupedShape, x, w, offsets, ws, out=None, stream=None):
     """Ragged products y[r] = w[e] x[r] for the rows r of each segment
     [offsets[e], offsets[e+1]) -> y [rows, n_out] (rows from offsets[groups] on
@@ -523,7 +535,7 @@ def grouped_matmul(shape: GroupedShape, x, w, offsets, ws, out=None, stream=None
     _need(x, "x", shape.dtype, (R, I))
     _need(w, "w", shape.dtype, (G, O, I))
     _need(offsets, "offsets", torch.int32, (G + 1,))
-    out = _out(out, "out", shape.dtype, (R, O), x.device)
+    out = _out(out, "out", shape.dtype, (R, O), x.device, stream)
     _on_current_device(x, w, offsets, ws, out)
     st = lib().moe_grouped_matmul(ctypes.byref(shape.c()), _ptr(x), _ptr(w), _ptr(offsets),
                                   _ptr(out), *_ws(ws), _stream(stream))
@@ -538,7 +550,7 @@ def grouped_matmul_dx(shape: GroupedShape, dy, w, offsets, ws, out=None, stream=
     _need(dy, "dy", shape.dtype, (R, O))
     _need(w, "w", shape.dtype, (G, O, I))
     _need(offsets, "offsets", torch.int32, (G + 1,))
-    out = _out(out, "out", shape.dtype, (R, I), dy.device)
+    out = _out(out, "out", shape.dtype, (R, I), dy.device, stream)
     _on_current_device(dy, w, offsets, ws, out)
     st = lib().moe_grouped_matmul_dx(ctypes.byref(shape.c()), _ptr(dy), _ptr(w),
                                      _ptr(offsets), _ptr(out), *_ws(ws), _stream(stream))
@@ -555,7 +567,7 @@ def grouped_matmul_dw(shape: GroupedShape, dy, x, offsets, ws, out=None, stream=
     _need(x, "x", shape.dtype, (R, I))
     _need(offsets, "offsets", torch.int32, (G + 1,))
     f32 = out is not None and out.dtype == torch.float32
-    out = _out(out, "out", torch.float32 if f32 else shape.dtype, (G, O, I), x.device)
+    out = _out(out, "out", torch.float32 if f32 else shape.dtype, (G, O, I), x.device, stream)
     _on_current_device(dy, x, offsets, ws, out)
     st = lib().moe_grouped_matmul_dw(ctypes.byref(shape.c()), _ptr(dy), _ptr(x),
                                      _ptr(offsets), _ptr(out), _DTYPE_CODE[out.dtype],
@@ -586,8 +598,8 @@ def combine_backward(shape: LayerShape, dout, x, y_perm, topk_idx, topk_gate, sl
     _need(topk_idx, "topk_idx", torch.int32, (T, k))
     _need(topk_gate, "topk_gate", torch.float32, (T, k))
     _need(slot_row, "slot_row", torch.int32, (T * k,))
-    dy_perm = _out(dy_perm, "dy_perm", shape.act_dtype, (T * k, d), x.device)
-    dgate = _out(dgate, "dgate", torch.float32, (T, k), x.device)
+    dy_perm = _out(dy_perm, "dy_perm", shape.act_dtype, (T * k, d), x.device, stream)
+    dgate = _out(dgate, "dgate", torch.float32, (T, k), x.device, stream)
     _on_current_device(dout, x, y_perm, topk_idx, topk_gate, slot_row, dy_perm, dgate)
     st = lib().moe_combine_backward(ctypes.byref(shape.c()), _ptr(dout), _ptr(x),
                                     _ptr(y_perm), _ptr(topk_idx), _ptr(topk_gate),
@@ -597,7 +609,7 @@ def combine_backward(shape: LayerShape, dout, x, y_perm, topk_idx, topk_gate, sl
     return dy_perm, dgate
 
 
-def _weight_grads(shape, dw_gate, dw_up, dw_down, device):
+def _weight_grads(shape, dw_gate, dw_up, dw_down, device, stream):
     """The experts' weight gradients (given or new) and their common type: the
     activation type unless the given ones are float32."""
     N, F, d = shape.n_routed, shape.ffn, shape.d
@@ -606,7 +618,7 @@ def _weight_grads(shape, dw_gate, dw_up, dw_down, device):
     if dtype not in (shape.act_dtype, torch.float32):
         raise ValueError(f"weight gradients: dtype {dtype}, expected {shape.act_dtype} "
                          "or torch.float32")
-    out = tuple(_out(t, n, dtype, s, device) for n, t, s in (
+    out = tuple(_out(t, n, dtype, s, device, stream) for n, t, s in (
         ("dw_gate", dw_gate, (N, F, d)), ("dw_up", dw_up, (N, F, d)),
         ("dw_down", dw_down, (N, d, F))))
     return out, _DTYPE_CODE[dtype]
@@ -630,8 +642,8 @@ def expert_ffn_backward(shape: LayerShape, x_perm, offsets, w_gate, w_up, w_down
     _need(offsets, "offsets", torch.int32, (shape.n_routed + 1,))
     _need_experts(shape, w_gate, w_up, w_down)
     _need(dy_perm, "dy_perm", shape.act_dtype, (T * k, d))
-    dx_perm = _out(dx_perm, "dx_perm", shape.act_dtype, (T * k, d), x_perm.device)
-    dws, code = _weight_grads(shape, dw_gate, dw_up, dw_down, x_perm.device)
+    dx_perm = _out(dx_perm, "dx_perm", shape.act_dtype, (T * k, d), x_perm.device, stream)
+    dws, code = _weight_grads(shape, dw_gate, dw_up, dw_down, x_perm.device, stream)
     _on_current_device(x_perm, offsets, w_gate, w_up, w_down, dy_perm, ws, dx_perm, *dws)
     st = lib().moe_expert_ffn_backward(ctypes.byref(shape.c()), _ptr(x_perm), _ptr(offsets),
                                        _ptr(w_gate), _ptr(w_up), _ptr(w_down), _ptr(dy_perm),
@@ -654,8 +666,8 @@ def input_backward(shape: LayerShape, dout, x, w_router, topk_idx, topk_gate, sl
     _need(slot_row, "slot_row", torch.int32, (T * k,))
     _need(dgate, "dgate", torch.float32, (T, k))
     _need(dx_perm, "dx_perm", shape.act_dtype, (T * k, d))
-    dx = _out(dx, "dx", shape.act_dtype, (T, d), x.device)
-    dw_router = _out(dw_router, "dw_router", torch.float32, (E, d), x.device)
+    dx = _out(dx, "dx", shape.act_dtype, (T, d), x.device, stream)
+    dw_router = _out(dw_router, "dw_router", torch.float32, (E, d), x.device, stream)
     _on_current_device(dout, x, w_router, topk_idx, topk_gate, slot_row, dgate, dx_perm,
                        ws, dx, dw_router)
     st = lib().moe_input_backward(ctypes.byref(shape.c()), _ptr(dout), _ptr(x),
@@ -685,9 +697,9 @@ def layer_backward(shape: LayerShape, dout, x, w_router, w_gate, w_up, w_down, t
         _need(offsets, "offsets", torch.int32, (N + 1,))
         _need(x_perm, "x_perm", shape.act_dtype, (T * k, d))
         _need(y_perm, "y_perm", shape.act_dtype, (T * k, d))
-    dx = _out(dx, "dx", shape.act_dtype, (T, d), x.device)
-    dw_router = _out(dw_router, "dw_router", torch.float32, (E, d), x.device)
-    dws, code = _weight_grads(shape, dw_gate, dw_up, dw_down, x.device)
+    dx = _out(dx, "dx", shape.act_dtype, (T, d), x.device, stream)
+    dw_router = _out(dw_router, "dw_router", torch.float32, (E, d), x.device, stream)
+    dws, code = _weight_grads(shape, dw_gate, dw_up, dw_down, x.device, stream)
     _on_current_device(dout, x, w_router, w_gate, w_up, w_down, topk_idx, topk_gate, offsets,
                        slot_row, x_perm, y_perm, ws, dx, dw_router, *dws)
     st = lib().moe_layer_backward(ctypes.byref(shape.c()), _ptr(dout), _ptr(x),

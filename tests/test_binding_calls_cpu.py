@@ -45,3 +45,68 @@ def test_every_call_with_an_empty_batch(relaxed):
     assert out.shape == (0, 64)
     moe.layer_forward_host(sh, x, w_r, b, wg, wg, wd, ws, torch.zeros(0, 64, dtype=bf),
                            stream=st)
+
+
+def test_new_outputs_come_from_the_memory_of_their_own_stream(monkeypatch):
+    """Every output that a call on another stream allocates is taken from that
+    stream's memory, and the current stream is noted as its user: otherwise an
+    output that the caller drops at once would be handed out again while the
+    call still writes it. Device tensors are stand-ins here."""
+    import contextlib
+    current, side = (types.SimpleNamespace(cuda_stream=n, name=n) for n in (1, 2))
+    active, made = [current], []
+
+    class Fake:
+        device = torch.device("cuda", 0)
+
+        def __init__(self, dtype=None):
+            self.dtype, self.owner, self.users = dtype, active[-1], []
+
+        def record_stream(self, stream):
+            self.users.append(stream)
+
+    def empty(*shape, dtype, device):
+        made.append(Fake(dtype))
+        return made[-1]
+
+    @contextlib.contextmanager
+    def on(stream):
+        active.append(stream)
+        yield
+        active.pop()
+
+    class Library:
+        def __getattr__(self, name):
+            return lambda *args: 2 if name == "moe_ep_local_experts" else 0
+
+    monkeypatch.setattr(torch, "empty", empty)
+    monkeypatch.setattr(torch.cuda, "stream", on)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: current)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device: side)
+    monkeypatch.setattr(moe, "lib", lambda: Library())
+    for name, value in (("_need", None), ("_on_current_device", None), ("_ptr", 0),
+                        ("_ws", (0, 0))):
+        monkeypatch.setattr(moe, name, lambda *a, value=value, **k: value)
+    sh = moe.LayerShape(T=4, d=64, n_routed=2, n_zero=1, top_k=2, ffn=64)
+    gs = moe.GroupedShape(8, 2, 16, 8)
+    t = Fake()
+    calls = [lambda **k: moe.route(sh, t, t, t, t, **k),
+             lambda **k: moe.dispatch(sh, t, t, t, **k),
+             lambda **k: moe.expert_ffn(sh, t, t, t, t, t, t, **k),
+             lambda **k: moe.combine(sh, t, t, t, t, t, **k),
+             lambda **k: moe.layer_forward(sh, t, t, t, t, t, t, t, **k),
+             lambda **k: moe.ep_plan(sh, 0, 2, t, **k),
+             lambda **k: moe.grouped_matmul(gs, t, t, t, t, **k),
+             lambda **k: moe.grouped_matmul_dx(gs, t, t, t, t, **k),
+             lambda **k: moe.grouped_matmul_dw(gs, t, t, t, t, **k),
+             lambda **k: moe.combine_backward(sh, t, t, t, t, t, t, **k),
+             lambda **k: moe.expert_ffn_backward(sh, t, t, t, t, t, t, t, **k),
+             lambda **k: moe.input_backward(sh, t, t, t, t, t, t, t, t, t, **k),
+             lambda **k: moe.layer_backward(sh, *[t] * 13, **k)]
+    for call in calls:
+        for stream in (current, side):
+            made.clear()
+            call(stream=stream)
+            assert made and all(m.owner is stream for m in made)
+            assert all((current in m.users) == (stream is side) for m in made)
+    assert active == [current]

@@ -434,6 +434,27 @@ def test_two_calls_at_once_on_two_streams():
         assert all(torch.equal(a, b) for a, b in zip(out, want))
 
 
+def test_an_output_dropped_at_once_is_not_handed_out_while_the_call_writes_it():
+    ls = moe.LayerShape(700, 512, 0, 8, 3, 8, BF)
+    x, dout, w_r, bias, *_ = weights(ls, 36)
+    g = torch.Generator().manual_seed(36)
+    idx, gate, slot_row, _ = ref.route_by_hand(700, 0, 8, 3, g)
+    idx, gate, slot_row, dgate = dev(idx, gate, slot_row, ref.random(g, 700, 3))
+    ws, rows = moe.alloc_backward_workspace(ls), torch.zeros(2100, 512, dtype=BF, device=DEV)
+    args = (ls, dout, x, w_r, idx, gate, slot_row, dgate, rows, ws)
+    want, _ = moe.input_backward(*args)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)  # about 10 ms: the call waits behind it
+    dx, dw = moe.input_backward(*args, stream=side)
+    del dw
+    # the current stream asks for the same size while the call is outstanding
+    mine = [torch.full((8, 512), 7.0, device=DEV) for _ in range(8)]
+    torch.cuda.synchronize()
+    assert all(bool((t == 7.0).all()) for t in mine) and torch.equal(dx, want)
+
+
 # ------------------------------------------- positions behind 2^31 elements --
 def test_grouped_rows_behind_two_to_the_31():
     R, I, O, G = 360_000, 6144, 64, 3  # x and dx hold 2.2 G elements
