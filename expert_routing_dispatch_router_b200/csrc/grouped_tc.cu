@@ -196,15 +196,6 @@ __device__ __forceinline__ void mma_stage(uint32_t d, uint64_t a, uint64_t b, ui
         : "memory");
 }
 
-// Arrive on another CTA's mbarrier where nothing in memory passes to it: an
-// accumulator has been read, which tcgen05.wait::ld has completed before. Release
-// at CTA scope; at cluster scope the arrive would first wait for every store this
-// warp has in flight.
-__device__ __forceinline__ void mbar_arrive_remote_light(uint32_t cluster_bar) {
-  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar)
-               : "memory");
-}
-
 // The same operations on one CTA or, from the leader, on a CTA pair. Copies of
 // a pair complete on the leader's barrier; commits arrive in both CTAs.
 template <bool PAIR>
@@ -293,7 +284,8 @@ __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatil
 }
 
 // The same with cluster-scope acquire, for a phase that the other CTA of the
-// pair completes after writing here.
+// pair takes part in: what it did before its arrival is ordered before what
+// follows here.
 __device__ __forceinline__ bool wait_bounded_cluster(uint32_t bar, uint32_t parity,
                                                      volatile int* abort_flag, int32_t* err) {
   if (ptx::mbar_try_wait_cluster(bar, parity)) return true;
@@ -308,6 +300,24 @@ __device__ __forceinline__ bool wait_bounded_cluster(uint32_t bar, uint32_t pari
       return false;
     }
   }
+}
+
+__device__ __forceinline__ bool wait_warp_cluster(uint32_t bar, uint32_t parity,
+                                                  volatile int* abort_flag, int32_t* err) {
+  return __all_sync(0xffffffffu, wait_bounded_cluster(bar, parity, abort_flag, err));
+}
+
+// Whether an mbarrier phase is complete, without waiting.
+__device__ __forceinline__ bool phase_done(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
 }
 
 // Bounded wait that ignores the stop flag (used while cleaning up).
@@ -332,12 +342,15 @@ constexpr uint32_t kCtlBytes = 320;
 // kRing slots in its own and its peer's shared memory; the other roles read
 // their units from there and arrive on the ring_empty barrier of their own CTA:
 // the MMA warp, the epilogue warps, a second producer if there is one (TWO), and
-// in the peer its producers and epilogue warps. A thread of the peer's otherwise
-// idle warp 1 passes the peer's takes on to the leader at cluster scope, so a
-// slot is stored to again only after everyone has read it. (Each reader could
-// arrive there itself; at cluster scope it would first wait for its stores in
-// flight, and at a narrower one its read would not be ordered before the next
-// store to the slot.) The last CTA (pair) to finish returns the counters to zero.
+// in the peer its producers and epilogue warps. The epilogue warps of both CTAs
+// arrive on the tempty barriers of their own CTA once they have read an
+// accumulator. A thread of the peer's otherwise idle warp 1 passes both on to the
+// leader with release at cluster scope, so a slot is stored to, and an accumulator
+// written, only after everyone has read it. (Each reader could arrive there
+// itself; at cluster scope it would first wait for its stores in flight, 1700 to
+// 2600 cycles, and at a narrower one its reads would not be ordered before what
+// the leader does next.) The last CTA (pair) to finish returns the counters to
+// zero.
 template <int S, bool PAIR, bool TWO>
 struct Control {
   uint32_t bars;
@@ -373,18 +386,53 @@ struct Control {
     ptx::mbar_arrive(ring_empty(r));
     return true;
   }
-  // The peer's warp 1 (one lane): once all of the peer has taken a unit, say so
-  // to the leader.
-  __device__ void relay_takes(int32_t* err) const {
-    for (int seq = 0;; ++seq) {
+  // The peer's warp 1 (one lane): once all of the peer has taken a unit, or has
+  // read an accumulator, say so to the leader. It waits for three barriers at
+  // once, so it asks them in turn. After the last take no accumulator is waited
+  // for any more: the peer's epilogue takes it when its last unit is done.
+  __device__ void relay(int32_t* err) const {
+    int seq = 0, u = 0;
+    bool published = false;  // unit seq is here, and not yet taken by all
+    uint32_t acc_par = 0;    // bit b: the phase of tempty(b) to come
+    uint64_t t0 = ptx::global_timer_ns();
+    for (int idle = 0;; ++idle) {
       const int r = seq % kRing;
       const uint32_t par = (uint32_t)(seq / kRing) & 1u;
-      if (!wait_bounded_cluster(ring_full(r), par, abort_flag, err)) return;
-      const int u = ring[r];
-      if (!wait_bounded(ring_empty(r), par, abort_flag, err)) return;
-      ptx::mbar_arrive_remote(ptx::map_to_rank(ring_empty(r), 0));
-      if (u < 0) return;
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+        if (phase_done(tempty(b), (acc_par >> b) & 1u)) {
+          ptx::mbar_arrive_remote(ptx::map_to_rank(tempty(b), 0));
+          acc_par ^= 1u << b;
+          idle = 0;
+        }
+      if (!published) {
+        if (phase_done(ring_full(r), par)) {
+          u = ring[r];
+          published = true;
+          idle = 0;
+        }
+      } else if (phase_done(ring_empty(r), par)) {
+        ptx::mbar_arrive_remote(ptx::map_to_rank(ring_empty(r), 0));
+        if (u < 0) return;
+        published = false;
+        ++seq;
+        idle = 0;
+      }
+      if (idle == 0) t0 = ptx::global_timer_ns();
+      if ((idle & 63) == 63) {
+        if (*abort_flag) return;
+        if (ptx::global_timer_ns() - t0 > kWaitLimitNs) {
+          *abort_flag = 1;
+          atomicCAS(err, 0, kErrWaitTimeout);
+          return;
+        }
+      }
     }
+  }
+  // The MMA warp's wait for accumulator b.
+  __device__ bool wait_released(int b, uint32_t parity, int32_t* err) const {
+    return PAIR ? wait_warp_cluster(tempty(b), parity, abort_flag, err)
+                : wait_warp(tempty(b), parity, abort_flag, err);
   }
   // Next unit for the producer warp: the leader publishes the one it claimed
   // before, then claims another (after the arrivals, which would wait for the
@@ -431,7 +479,8 @@ struct Control {
       }
       for (int b = 0; b < 2; ++b) {
         ptx::mbar_init(tfull(b), 1);
-        ptx::mbar_init(tempty(b), PAIR ? 2 * kEpiWarps : kEpiWarps);
+        // the epilogue; in the leader also the relay
+        ptx::mbar_init(tempty(b), kEpiWarps + (PAIR && Cg<PAIR>::rank() == 0 ? 1 : 0));
       }
       ptx::mbar_init(mma_done(), 1);
       for (int r = 0; r < kRing; ++r) {
@@ -450,12 +499,7 @@ struct Control {
   __device__ void release(int b, int lane) const {
     ptx::tc_fence_before();
     __syncwarp();
-    if (lane == 0) {
-      if (PAIR && Cg<PAIR>::rank() != 0)
-        mbar_arrive_remote_light(ptx::map_to_rank(tempty(b), 0));
-      else
-        ptx::mbar_arrive(tempty(b));
-    }
+    if (lane == 0) ptx::mbar_arrive(tempty(b));
   }
   // After an abort: let the copies that were issued land before the CTA goes.
   // The leader sees them on its full barriers; the peer's complete there too.
@@ -712,11 +756,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok || u < 0) break;
         const RowUnit un = row_unit<BN>(u, s_tile, s_off, args.groups, m_tiles);
         const int n0 = mma_rows(un.n, 0), n1 = PAIR ? mma_rows(un.n, 1) : 0;
-        if (!(ok = wait_warp(ctl.tempty(slot & 1), ((slot >> 1) & 1u) ^ 1u, ctl.abort_flag,
-                             args.err)))
-          break;
-        if (n1 > 0 && !(ok = wait_warp(ctl.tempty((slot + 1) & 1), (((slot + 1) >> 1) & 1u) ^ 1u,
-                                       ctl.abort_flag, args.err)))
+        if (!(ok = ctl.wait_released(slot & 1, ((slot >> 1) & 1u) ^ 1u, args.err))) break;
+        if (n1 > 0 && !(ok = ctl.wait_released((slot + 1) & 1, (((slot + 1) >> 1) & 1u) ^ 1u,
+                                               args.err)))
           break;
         ptx::tc_fence_after();
         const uint32_t i0 = ptx::idesc_bf16_f32(BM * C::kCtas, n0) | kFlags;
@@ -755,7 +797,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
     } else {
-      if (lane == 0) ctl.relay_takes(args.err);
+      if (lane == 0) ctl.relay(args.err);
       __syncwarp();
     }
   } else {
@@ -1100,7 +1142,7 @@ __global__ void __launch_bounds__(kDwThreads, 1)
         const int sa0 = sa;
         const uint32_t pa0 = pa;
         for (int jt = un.jt0; jt < un.jt1 && ok; ++jt) {
-          if (!(ok = wait_warp(ctl.tempty(acc), acc_phase ^ 1u, ctl.abort_flag, args.err))) break;
+          if (!(ok = ctl.wait_released(acc, acc_phase ^ 1u, args.err))) break;
           ptx::tc_fence_after();
           const uint32_t d0 = tmem_base + (uint32_t)acc * kAccStride;
           const bool load_a = jt == un.jt0 || !keep;
@@ -1150,7 +1192,7 @@ __global__ void __launch_bounds__(kDwThreads, 1)
       }
       __syncwarp();
     } else {
-      if (lane == 0) ctl.relay_takes(args.err);
+      if (lane == 0) ctl.relay(args.err);
       __syncwarp();
     }
   } else {

@@ -397,3 +397,22 @@ def test_adamw_reads_gradients_where_they_lie(host_adamw):
     step()
     assert opt._kept[0][0] is captured and opt._kept[0][1][2].data_ptr() == other.data_ptr()
     assert opt._table is not captured and len(opt._kept) == 1
+
+
+# ------------------------------------------------------------- the sources --
+def test_arrivals_on_another_cta_release_at_cluster_scope():
+    """At a narrower scope nothing that a thread did before its arrival is
+    ordered before what the other CTA does after its wait, and two CTAs of a pair
+    hand accumulators and unit ids to each other by such arrivals."""
+    import glob
+    import os
+    import re
+    csrc = os.path.join(os.path.dirname(moe.__file__), "csrc")
+    seen = 0
+    for path in sorted(glob.glob(os.path.join(csrc, "*.cu*"))):
+        with open(path) as f:
+            text = f.read()
+        for op in re.findall(r"mbarrier\.arrive[\w.:]*shared::cluster[\w.:]*", text):
+            assert op.startswith("mbarrier.arrive.release.cluster."), (path, op)
+            seen += 1
+    assert seen > 0
