@@ -121,31 +121,53 @@ bool disjoint(const Span (&s)[N]) {
 }
 
 // ---- device helpers ----
+// An offset within the row buffers.
+__device__ __forceinline__ int32_t clamp_offset(int32_t o, int64_t rows) {
+  return o < 0 ? 0 : (o > rows ? (int32_t)rows : o);
+}
 // Segment table of a block in shared memory: s_off[0..n] the row offsets,
 // s_tile[0..n] the prefix sums of the segments' tiles of `tile` rows, where up
-// to `slack` rows behind the last full tile count as part of it. Offsets are clamped to
-// [0, rows] and to be non-decreasing, so no table sends a kernel outside its
-// buffers. All THREADS threads call it; s_warp holds 32 ints. Each thread
-// takes `per` consecutive segments.
+// to `slack` rows behind the last full tile count as part of it. Offsets are
+// clamped to [0, rows] and replaced by their running maximum, so no table sends a
+// kernel outside its buffers, gives a row to two segments, or has more tiles than
+// the rows do (ASCENDING: they come from a sort and do not fall). All THREADS
+// threads call it; s_warp holds 32 ints. Each thread takes `per` consecutive
+// segments.
 __device__ __forceinline__ int32_t segment_tiles(int32_t rows, int tile, int slack) {
   if (rows <= 0) return 0;
   return rows <= tile + slack ? 1 : (rows - slack + tile - 1) / tile;
 }
-template <int THREADS>
+// The table of offsets that fall, by one thread. Looking whether any falls takes
+// the CUDA-core kernels 0.2 to 1 us (the tiny float layer's backward 52 -> 55 us),
+// the others nothing that shows.
+static __device__ __noinline__ void raise_segments(int n, int tile, int slack, int32_t* s_off,
+                                                   int32_t* s_tile) {
+  if (threadIdx.x == 0) {
+    s_tile[0] = 0;
+    for (int e = 0; e < n; ++e) {
+      s_off[e + 1] = max(s_off[e + 1], s_off[e]);
+      s_tile[e + 1] = s_tile[e] + segment_tiles(s_off[e + 1] - s_off[e], tile, slack);
+    }
+  }
+  __syncthreads();
+}
+template <int THREADS, bool ASCENDING = false>
 __device__ __forceinline__ void segment_table(const int32_t* __restrict__ offsets, int n,
                                               int64_t rows, int tile, int slack, int32_t* s_off,
                                               int32_t* s_tile, int32_t* s_warp) {
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   const int per = (n + THREADS - 1) / THREADS;
-  for (int i = threadIdx.x; i <= n; i += THREADS) {
-    const int32_t o = offsets[i];
-    s_off[i] = o < 0 ? 0 : (o > rows ? (int32_t)rows : o);
-  }
+  for (int i = threadIdx.x; i <= n; i += THREADS) s_off[i] = clamp_offset(offsets[i], rows);
   __syncthreads();
   int32_t sum = 0;
+  bool falls = false;
   for (int q = 0; q < per; ++q) {
     const int e = threadIdx.x * per + q;
-    if (e < n) sum += segment_tiles(s_off[e + 1] - s_off[e], tile, slack);
+    if (e < n) {
+      const int32_t len = s_off[e + 1] - s_off[e];
+      falls |= len < 0;
+      sum += segment_tiles(len, tile, slack);
+    }
   }
   int32_t incl = sum;
 #pragma unroll
@@ -154,7 +176,12 @@ __device__ __forceinline__ void segment_table(const int32_t* __restrict__ offset
     if (lane >= off) incl += o;
   }
   if (lane == 31) s_warp[wid] = incl;
-  __syncthreads();
+  if (ASCENDING) {
+    __syncthreads();
+  } else if (__syncthreads_or(falls)) {
+    raise_segments(n, tile, slack, s_off, s_tile);
+    return;
+  }
   int32_t before = incl - sum;
   for (int w = 0; w < wid; ++w) before += s_warp[w];
   for (int q = 0; q < per; ++q) {

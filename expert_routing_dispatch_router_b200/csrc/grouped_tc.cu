@@ -978,10 +978,11 @@ __host__ __device__ __forceinline__ int dw_runs(int n_in) {
   return (nj + DwCfg::kRun - 1) / DwCfg::kRun;
 }
 
-// The offsets are read where a unit is taken up (clamped as segment_table
-// does); shared memory is all operand slots.
+// The offsets are read where a unit is taken up (shared memory is all operand
+// slots), clamped and by their running maximum as in segment_table. That needs
+// the offsets before only where they do not ascend anyway (!ascending).
 __device__ __forceinline__ DwUnit dw_unit(int u, const int* first, const DwMaps& maps,
-                                          const DwArgs& args) {
+                                          const DwArgs& args, bool ascending) {
   DwUnit un;
   un.job = u >= first[2] ? 2 : (u >= first[1] ? 1 : 0);
   const DwJob& j = maps.job[un.job];
@@ -992,10 +993,11 @@ __device__ __forceinline__ DwUnit dw_unit(int u, const int* first, const DwMaps&
   un.e = v / runs / ni;
   un.jt0 = nj * run / runs;
   un.jt1 = nj * (run + 1) / runs;
-  const int rows = (int)args.rows;
-  const int lo = __ldg(args.offsets + un.e), hi = __ldg(args.offsets + un.e + 1);
-  un.row0 = lo < 0 ? 0 : (lo > rows ? rows : lo);
-  const int end = hi < 0 ? 0 : (hi > rows ? rows : hi);
+  un.row0 = clamp_offset(__ldg(args.offsets + un.e), args.rows);
+  if (!ascending)
+    for (int i = 0; i < un.e; ++i)
+      un.row0 = max(un.row0, clamp_offset(__ldg(args.offsets + i), args.rows));
+  const int end = clamp_offset(__ldg(args.offsets + un.e + 1), args.rows);
   un.n_rows = end > un.row0 ? end - un.row0 : 0;
   return un;
 }
@@ -1060,8 +1062,12 @@ __global__ void __launch_bounds__(kDwThreads, 1)
   const uint32_t rank = G::rank();
   griddep_wait();
   griddep_launch_dependents();
+  bool falls = false;
+  for (int i = threadIdx.x; i < args.groups; i += kDwThreads)
+    falls |= clamp_offset(__ldg(args.offsets + i + 1), args.rows) <
+             clamp_offset(__ldg(args.offsets + i), args.rows);
   ptx::tc_fence_before();
-  __syncthreads();
+  const bool ascending = !__syncthreads_or(falls);
   G::sync_all();
   ptx::tc_fence_after();
   const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(ctl.tmem_slot);
@@ -1094,7 +1100,7 @@ __global__ void __launch_bounds__(kDwThreads, 1)
       ok = load_b ? ctl.take_warp(seq, &u, args.err)
                   : ctl.next(seq, total, args.counters, &claimed, &u, args.err);
       if (!ok || u < 0) break;
-      const DwUnit un = dw_unit(u, first_unit, maps, args);
+      const DwUnit un = dw_unit(u, first_unit, maps, args, ascending);
       const DwJob& job = maps.job[un.job];
       const CUtensorMap* m = load_b ? job.b : job.a;
       const bool wide = (load_b ? job.n_in : job.n_out) % 64 == 0;
@@ -1136,7 +1142,7 @@ __global__ void __launch_bounds__(kDwThreads, 1)
       for (int seq = 0, u; ok; ++seq) {
         ok = ctl.take_warp(seq, &u, args.err);
         if (!ok || u < 0) break;
-        const DwUnit un = dw_unit(u, first_unit, maps, args);
+        const DwUnit un = dw_unit(u, first_unit, maps, args, ascending);
         if (un.n_rows == 0) continue;  // the epilogue writes zeros by itself
         const bool keep = un.n_rows <= SA * BK;
         const int sa0 = sa;
@@ -1209,7 +1215,7 @@ __global__ void __launch_bounds__(kDwThreads, 1)
     uint32_t acc_phase = 0;
     bool ok = true;
     for (int seq = 0, u; ok && ctl.take_warp(seq, &u, args.err) && u >= 0; ++seq) {
-      const DwUnit un = dw_unit(u, first_unit, maps, args);
+      const DwUnit un = dw_unit(u, first_unit, maps, args, ascending);
       const DwJob& job = maps.job[un.job];
       const int n_out = job.n_out, n_in = job.n_in;
       const int row = (un.it * 2 + (int)rank) * BM + ew * 32;

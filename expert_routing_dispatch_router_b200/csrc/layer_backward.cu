@@ -215,8 +215,10 @@ __global__ void __launch_bounds__(256)
                            float* du) {
   griddep_wait();
   griddep_launch_dependents();
-  int64_t R = offsets[N];
-  if (R > rows) R = rows;
+  // the rows end at the largest offset (segment_table's running maximum)
+  int32_t end = 0;
+  for (int i = threadIdx.x & 31; i <= N; i += 32) end = max(end, clamp_offset(offsets[i], rows));
+  const int64_t R = __reduce_max_sync(0xffffffffu, end);
   for (int64_t i = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) * 4; i < R * F;
        i += (int64_t)gridDim.x * blockDim.x * 4) {
     const float4 av = *reinterpret_cast<const float4*>(da + i);
@@ -292,7 +294,7 @@ __global__ void __launch_bounds__(kDwThreads)
   __shared__ float s_dl[kDwChunk];
   griddep_wait();
   griddep_launch_dependents();
-  segment_table<kDwThreads>(offsets, E, slots, kDwChunk, 0, s_off, s_tile, s_warp);
+  segment_table<kDwThreads, true>(offsets, E, slots, kDwChunk, 0, s_off, s_tile, s_warp);
   if (blockIdx.x == 0)
     for (int i = threadIdx.x; i <= E; i += kDwThreads) chunk_start[i] = s_tile[i];
   const int cb = (int)((d + kDwThreads * V - 1) / (kDwThreads * V));

@@ -286,8 +286,8 @@ moe_status_t moe_bias_pid_update(const moe_config_t* cfg, const int32_t* counts,
  *  - No rows: a call without rows writes what a sum over nothing is, zeros in
  *    its weight gradients, and needs only those pointers (aligned); outputs
  *    with one row per token or slot are empty.
- *  - Offsets outside [0, rows] are taken as the nearest bound, and a segment
- *    that ends before it starts as empty.
+ *  - Offsets outside [0, rows] are taken as the nearest bound, and one below an
+ *    earlier one as that: its segment is empty, and no row belongs to two.
  *  - Sums run in fp32 in an order that does not depend on thread timing. A
  *    result is rounded once, when it is stored; h and the gradients of the
  *    pre-activations are also rounded to the activation type, as h is in the

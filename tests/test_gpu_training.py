@@ -125,6 +125,56 @@ def test_grouped_offsets_outside_the_rows_stay_in_bounds():
         assert int(dw[1].count_nonzero()) == 0
 
 
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("off", [(-5, 30, 20, 900), (0, 300, 0, 300, 0, 300, 0),
+                                 (250, 10, 260, 255, 270, 2 ** 31 - 1), (0, 290, 40, 120, 295)],
+                         ids=str)
+def test_grouped_offsets_that_fall_give_no_row_to_two_groups(off, dtype):
+    # an offset counts as the largest up to it, within the rows; rows before
+    # the first segment and behind the last are left as they were
+    R, I, O, G = 300, 136, 72, len(off) - 1
+    ends = torch.tensor(off).clamp(0, R).cummax(0).values.int()
+    sh = moe.GroupedShape(R, G, I, O, dtype)
+    ws = moe.alloc_grouped_workspace(sh)
+    g = torch.Generator().manual_seed(9)
+    x, dy, w = (ref.random(g, *s, dtype=dtype) for s in ((R, I), (R, O), (G, O, I)))
+    y, dx = (torch.full((R, n), 7.0, dtype=dtype, device=DEV) for n in (O, I))
+    offd = torch.tensor(off, dtype=torch.int32, device=DEV)
+    xd, dyd, wd = dev(x, dy, w)
+    for _ in range(3):
+        moe.grouped_matmul(sh, xd, wd, offd, ws, out=y)
+        moe.grouped_matmul_dx(sh, dyd, wd, offd, ws, out=dx)
+        dw = moe.grouped_matmul_dw(sh, dyd, xd, offd, ws)
+    assert moe.read_device_error(ws) == 0
+    x, dy, w = x.double(), dy.double(), w.double()
+    for e, lo, hi in ref.segments(ends):
+        ref.check(y[lo:hi], *ref.mm(x[lo:hi], w[e].T), dtype, f"y of {e}")
+        ref.check(dx[lo:hi], *ref.mm(dy[lo:hi], w[e]), dtype, f"dx of {e}")
+        ref.check(dw[e], *ref.mm(dy[lo:hi].T, x[lo:hi]), dtype, f"dw of {e}")
+    for t in (y, dx):
+        assert bool((t[:int(ends[0])] == 7.0).all()) and bool((t[int(ends[-1]):] == 7.0).all())
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+def test_expert_ffn_backward_with_offsets_that_fall(dtype):
+    T, d, N, F = 90, 64, 4, 40
+    off = torch.tensor([0, 70, 30, 85, 20], dtype=torch.int32)  # as 0, 70, 70, 85, 85
+    g = torch.Generator().manual_seed(12)
+    mk = lambda *s, sc=1.0: ref.random(g, *s, dtype=dtype, scale=sc)  # noqa: E731
+    x, dy = mk(T, d), mk(T, d)
+    wg, wu, wd = (mk(*s, sc=d ** -0.5) for s in ((N, F, d), (N, F, d), (N, d, F)))
+    sh = moe.LayerShape(T, d, N, 1, 1, F, dtype)
+    ws = moe.alloc_backward_workspace(sh)
+    dx = torch.full(x.shape, 7.0, dtype=dtype, device=DEV)
+    got = moe.expert_ffn_backward(sh, *dev(x, off, wg, wu, wd, dy), ws, dx_perm=dx)
+    assert moe.read_device_error(ws) == 0
+    want = ref.ffn_backward(x[:85], off.cummax(0).values, wg, wu, wd, dy[:85], dtype)
+    ref.check(got[0][:85], *want[0], dtype, "dx")
+    assert bool((got[0][85:] == 7.0).all())
+    for a, (v, err) in zip(got[1:], want[1:]):
+        ref.check(a, v, err, dtype, "weight gradient")
+
+
 # ------------------------------------------------------- experts' backward --
 def ffn_case(T, d, N, Z, k, F, dtype, seed, popular=None):
     g = torch.Generator().manual_seed(seed)
