@@ -956,7 +956,13 @@ struct DwArgs {
 // panel in shared memory for the whole run, so only x streams: half the
 // operand bytes of loading both, which is what bounds short segments (their
 // operands come from L2 at about 64 bytes a clock and SM).
+// The tensor cores cut where they add to an accumulator, so a chain over all rows
+// of a long segment drifts when its terms have one sign: 5e-4 of the sum at 400000
+// rows. A tile therefore starts a new accumulator every kChain rows (64 additions
+// of 16 rows), and the epilogue adds them in registers, in order and rounding. It
+// does so under the next chain's products.
 struct DwCfg {
+  static constexpr int kChain = 1024;
   static constexpr int kRun = 8;
   static constexpr int kASlots = 5, kBSlots = 7;
   static constexpr uint32_t kSlotBytes = 2 * kBlockBytes;  // 128 columns x 64 rows
@@ -966,6 +972,7 @@ struct DwCfg {
   static constexpr uint32_t kBarOff = kOutOff + kEpiWarps * kOutBuf;
   static constexpr uint32_t kSmemBytes = 1024 + kBarOff + kCtlBytes;
   static_assert(kSmemBytes <= 232448, "shared memory of a CTA");
+  static_assert(kChain % BK == 0 && kASlots * BK <= kChain, "a kept panel is one chain");
 };
 
 struct DwUnit {
@@ -1148,47 +1155,50 @@ __global__ void __launch_bounds__(kDwThreads, 1)
         const int sa0 = sa;
         const uint32_t pa0 = pa;
         for (int jt = un.jt0; jt < un.jt1 && ok; ++jt) {
-          if (!(ok = ctl.wait_released(acc, acc_phase ^ 1u, args.err))) break;
-          ptx::tc_fence_after();
-          const uint32_t d0 = tmem_base + (uint32_t)acc * kAccStride;
           const bool load_a = jt == un.jt0 || !keep;
           const bool free_a = jt == un.jt1 - 1 || !keep;
           if (keep) {  // each tile of the run reads the same slots
             sa = sa0;
             pa = pa0;
           }
-          for (int k0 = 0; k0 < un.n_rows; k0 += BK) {
-            if (load_a && !(ok = wait_warp(ctl.full(sa), pa, ctl.abort_flag, args.err))) break;
-            if (!(ok = wait_warp(ctl.full(SA + sb), pb, ctl.abort_flag, args.err))) break;
+          for (int c0 = 0; c0 < un.n_rows && ok; c0 += C::kChain) {
+            if (!(ok = ctl.wait_released(acc, acc_phase ^ 1u, args.err))) break;
             ptx::tc_fence_after();
-            const int left = un.n_rows - k0;
-            if (elected) {
-              const uint64_t a = hi | ((sbase + sa * C::kSlotBytes) >> 4);
-              const uint64_t b = hi | ((sbase + C::kBOff + sb * C::kSlotBytes) >> 4);
-              if (left > BK - 16) {
-                mma_stage<true, 128, 128>(d0, a, b, idesc, k0 != 0 ? 1u : 0u);
-              } else {
-                for (int kk = 0; kk * 16 < left; ++kk)
-                  G::mma(d0, a + kk * 128, b + kk * 128, idesc, (k0 | kk) != 0 ? 1u : 0u);
+            const uint32_t d0 = tmem_base + (uint32_t)acc * kAccStride;
+            const int rows = un.n_rows - c0 < C::kChain ? un.n_rows - c0 : C::kChain;
+            for (int k0 = 0; k0 < rows; k0 += BK) {
+              if (load_a && !(ok = wait_warp(ctl.full(sa), pa, ctl.abort_flag, args.err))) break;
+              if (!(ok = wait_warp(ctl.full(SA + sb), pb, ctl.abort_flag, args.err))) break;
+              ptx::tc_fence_after();
+              const int left = rows - k0;
+              if (elected) {
+                const uint64_t a = hi | ((sbase + sa * C::kSlotBytes) >> 4);
+                const uint64_t b = hi | ((sbase + C::kBOff + sb * C::kSlotBytes) >> 4);
+                if (left > BK - 16) {
+                  mma_stage<true, 128, 128>(d0, a, b, idesc, k0 != 0 ? 1u : 0u);
+                } else {
+                  for (int kk = 0; kk * 16 < left; ++kk)
+                    G::mma(d0, a + kk * 128, b + kk * 128, idesc, (k0 | kk) != 0 ? 1u : 0u);
+                }
+                G::commit(ctl.empty(SA + sb));
+                if (free_a) G::commit(ctl.empty(sa));
               }
-              G::commit(ctl.empty(SA + sb));
-              if (free_a) G::commit(ctl.empty(sa));
+              issued = true;
+              if (++sa == SA) {
+                sa = 0;
+                pa ^= 1u;
+              }
+              if (++sb == SB) {
+                sb = 0;
+                pb ^= 1u;
+              }
             }
-            issued = true;
-            if (++sa == SA) {
-              sa = 0;
-              pa ^= 1u;
+            if (!ok) break;
+            if (elected) G::commit(ctl.tfull(acc));
+            if (++acc == 2) {
+              acc = 0;
+              acc_phase ^= 1u;
             }
-            if (++sb == SB) {
-              sb = 0;
-              pb ^= 1u;
-            }
-          }
-          if (!ok) break;
-          if (elected) G::commit(ctl.tfull(acc));
-          if (++acc == 2) {
-            acc = 0;
-            acc_phase ^= 1u;
           }
         }
       }
@@ -1220,31 +1230,28 @@ __global__ void __launch_bounds__(kDwThreads, 1)
       const int n_out = job.n_out, n_in = job.n_in;
       const int row = (un.it * 2 + (int)rank) * BM + ew * 32;
       for (int jt = un.jt0; jt < un.jt1; ++jt) {
-        uint32_t w[kPieces][32];
-        if (un.n_rows > 0) {
+        float sum[4][32];  // this lane's row, 128 columns
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int c = 0; c < 32; ++c) sum[q][c] = 0.f;
+        for (int c0 = 0; c0 < un.n_rows; c0 += C::kChain) {
           ok = __all_sync(0xffffffffu,
                           wait_bounded(ctl.tfull(acc), acc_phase, ctl.abort_flag, args.err));
           if (!ok) break;
           ptx::tc_fence_after();
           const uint32_t tb = tmem_base + (static_cast<uint32_t>(ew * 32) << 16) +
                               (uint32_t)acc * kAccStride + (uint32_t)eh * 128u;
+          if (c0 == 0) {
+            ptx::tmem_ld32x2(tb, tb + 32, sum[0], sum[1]);
+            ptx::tmem_ld32x2(tb + 64, tb + 96, sum[2], sum[3]);
+          } else {
 #pragma unroll
-          for (int q = 0; q < kPieces; ++q) {
-            float g[32];
-            if (OUT_F32) {
-              ptx::tmem_ld32(tb + 32 * q, g);
+            for (int q = 0; q < 8; ++q) {
+              float g[16];
+              ptx::tmem_ld16(tb + 16 * q, g);
 #pragma unroll
-              for (int c = 0; c < 32; ++c) w[q][c] = __float_as_uint(g[c]);
-            } else {
-              float v[32];
-              ptx::tmem_ld32x2(tb + 64 * q, tb + 64 * q + 32, g, v);
-#pragma unroll
-              for (int c = 0; c < 16; ++c) {
-                const __nv_bfloat162 lo = __floats2bfloat162_rn(g[2 * c], g[2 * c + 1]);
-                const __nv_bfloat162 hi = __floats2bfloat162_rn(v[2 * c], v[2 * c + 1]);
-                w[q][c] = *reinterpret_cast<const uint32_t*>(&lo);
-                w[q][16 + c] = *reinterpret_cast<const uint32_t*>(&hi);
-              }
+              for (int c = 0; c < 16; ++c) sum[q >> 1][16 * (q & 1) + c] += g[c];
             }
           }
           ctl.release(acc, lane);
@@ -1252,12 +1259,8 @@ __global__ void __launch_bounds__(kDwThreads, 1)
             acc = 0;
             acc_phase ^= 1u;
           }
-        } else {
-#pragma unroll
-          for (int q = 0; q < kPieces; ++q)
-#pragma unroll
-            for (int c = 0; c < 32; ++c) w[q][c] = 0u;
         }
+        if (!ok) break;
 #pragma unroll
         for (int q = 0; q < kPieces; ++q) {
           const int col = jt * 256 + eh * 128 + q * kWidth;
@@ -1265,9 +1268,22 @@ __global__ void __launch_bounds__(kDwThreads, 1)
           if (lane == 0) store_wait_read<0>();  // the last store has read the buffer
           __syncwarp();
 #pragma unroll
-          for (int c = 0; c < 8; ++c)
-            st_shared_v4(buf + lane * 128u + (uint32_t)((c ^ (lane & 7)) << 4), w[q][4 * c],
-                         w[q][4 * c + 1], w[q][4 * c + 2], w[q][4 * c + 3]);
+          for (int c = 0; c < 8; ++c) {
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              if (OUT_F32) {
+                w[i] = __float_as_uint(sum[q][4 * c + i]);
+              } else {
+                const int at = 64 * q + 8 * c + 2 * i;
+                const __nv_bfloat162 p =
+                    __floats2bfloat162_rn(sum[at >> 5][at & 31], sum[at >> 5][(at & 31) + 1]);
+                w[i] = *reinterpret_cast<const uint32_t*>(&p);
+              }
+            }
+            st_shared_v4(buf + lane * 128u + (uint32_t)((c ^ (lane & 7)) << 4), w[0], w[1], w[2],
+                         w[3]);
+          }
           fence_async_smem();
           __syncwarp();
           if (lane == 0) {

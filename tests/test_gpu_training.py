@@ -101,6 +101,29 @@ def test_grouped_values_of_one_group_stay_in_it(n_in, n_out, dtype):
     check_grouped((33, 1, 0, 90), n_in, n_out, dtype, slack=64, seed=5, spoil=3)
 
 
+@pytest.mark.parametrize("dw_dtype", [F32, BF], ids=["f32", "bf16"])
+def test_grouped_weight_gradient_of_a_long_segment_does_not_drift(dw_dtype):
+    # terms of one sign, where sums that cut instead of rounding drift with
+    # every step: 1024 rows are one chain of sums (every addition cut, 2^-23 of
+    # the sum so far), and the chains' sums are added rounding (2^-24 each)
+    sizes, I, O = (400_017, 1, 1023, 1025, 5000), 136, 72
+    R = sum(sizes)
+    g = torch.Generator(device=DEV).manual_seed(51)
+    x, dy = ((torch.rand(R, n, generator=g, device=DEV) * 0.5 + 0.5).to(BF) for n in (I, O))
+    off = dev(ref.offsets_of(sizes))
+    sh = moe.GroupedShape(R, len(sizes), I, O)
+    ws = moe.alloc_grouped_workspace(sh)
+    out = torch.empty(len(sizes), O, I, dtype=dw_dtype, device=DEV)
+    moe.grouped_matmul_dw(sh, dy, x, off, ws, out=out)
+    assert moe.read_device_error(ws) == 0
+    for e, lo, hi in ref.segments(off):
+        want = sum(dy[i:min(i + 50_000, hi)].double().T @ x[i:min(i + 50_000, hi)].double()
+                   for i in range(lo, hi, 50_000))
+        n = hi - lo
+        bound = (min(n, 1024) * ref.U + (n // 1024 + 1) * ref.U / 2) * want
+        ref.check(out[e], want.cpu(), bound.cpu(), dw_dtype, f"dw of {n} rows")
+
+
 def test_grouped_large_batches():
     # enough rows per group for the largest tiles of every path
     check_grouped((1030, 511, 0, 1290), 512, 768, BF, slack=100, seed=6)
