@@ -60,6 +60,11 @@ cudaError_t launch_swiglu_backward_tc(const GroupedShape& g, const void* x, cons
 // all rows of a segment, about 40 ns a row; at this limit that is a third of the
 // time after which a wait for the next unit gives up.
 constexpr int64_t kMaxGroupedRows = 1ll << 24;
+// Sizes of a matrix. A row product is one chain of sums over its contraction,
+// which drifts where the tensor cores cut: 1.3e-3 of a sum of terms of one sign at
+// this limit, a third of bf16's half step. A unit of it also stays far inside the
+// wait's bound, and the numbers of column tiles within 32 bits when multiplied.
+constexpr int64_t kMaxGroupedDim = 1ll << 20;
 // Whether a product keeps to that, and its unit numbers to 32 bits.
 bool grouped_fits(int64_t rows, int64_t groups, int64_t n_in, int64_t n_out);
 

@@ -294,7 +294,8 @@ cudaError_t launch_grouped_jobs(const GroupedShape& g, const GroupedJob* jobs, i
 bool grouped_fits(int64_t rows, int64_t groups, int64_t n_in, int64_t n_out) {
   const int64_t row_units = (rows / 64 + groups) * ((n_in > n_out ? n_in : n_out) / 64 + 1);
   const int64_t dw_units = groups * (n_in / 64 + 1) * (n_out / 64 + 1);
-  return row_units < (1ll << 31) && dw_units < (1ll << 31) && rows <= kMaxGroupedRows;
+  return row_units < (1ll << 31) && dw_units < (1ll << 31) && rows <= kMaxGroupedRows &&
+         n_in <= kMaxGroupedDim && n_out <= kMaxGroupedDim;
 }
 
 }  // namespace moe

@@ -303,8 +303,8 @@ moe_status_t moe_bias_pid_update(const moe_config_t* cfg, const int32_t* counts,
  *  read into a result nor written. A segment without rows gives a zero dw[e].
  *  dtype is the type of every tensor but the offsets; dw_dtype may also be
  *  MOE_F32 for bf16 operands (the fp32 sums as they are).
- *  Limits: rows <= 2^24, 1 <= groups <= 1024, n_in and n_out multiples of 8, and
- *  (rows / 64 + groups) * (max(n_in, n_out) / 64 + 1) and
+ *  Limits: rows <= 2^24, 1 <= groups <= 1024, n_in and n_out multiples of 8 up to
+ *  2^20, and (rows / 64 + groups) * (max(n_in, n_out) / 64 + 1) and
  *  groups * (n_in / 64 + 1) * (n_out / 64 + 1) below 2^31.
  *  The workspace holds the error word and small counters that the kernels
  *  return to zero: moe_grouped_workspace_size bytes, 256-byte aligned, zero

@@ -124,6 +124,29 @@ def test_grouped_weight_gradient_of_a_long_segment_does_not_drift(dw_dtype):
         ref.check(out[e], want.cpu(), bound.cpu(), dw_dtype, f"dw of {n} rows")
 
 
+@pytest.mark.parametrize("n_in,n_out", [(1 << 20, 8), (8, 1 << 20)])
+def test_grouped_widest_matrices(n_in, n_out):
+    # terms of one sign; a product of 2^20 terms is 2^16 additions of 16, each
+    # cut by up to 2^-23 of a sum so far that is half the last one on average
+    R, off = 5, torch.tensor([0, 2, 5], dtype=torch.int32)
+    g = torch.Generator().manual_seed(52)
+    x, dy, w = ((torch.rand(*s, generator=g) * 0.5 + 0.5).to(BF)
+                for s in ((R, n_in), (R, n_out), (2, n_out, n_in)))
+    sh = moe.GroupedShape(R, 2, n_in, n_out)
+    ws = moe.alloc_grouped_workspace(sh)
+    xd, dyd, wd, offd = dev(x, dy, w, off)
+    y = moe.grouped_matmul(sh, xd, wd, offd, ws)
+    dx = moe.grouped_matmul_dx(sh, dyd, wd, offd, ws)
+    dw = moe.grouped_matmul_dw(sh, dyd, xd, offd, ws)
+    assert moe.read_device_error(ws) == 0
+    x, dy, w = x.double(), dy.double(), w.double()
+    for e, lo, hi in ref.segments(off):
+        for got, want, terms in ((y[lo:hi], x[lo:hi] @ w[e].T, n_in),
+                                 (dx[lo:hi], dy[lo:hi] @ w[e], n_out),
+                                 (dw[e], dy[lo:hi].T @ x[lo:hi], 16)):
+            ref.check(got, want, max(terms // 16, 16) * ref.U / 2 * want, BF, f"{terms} terms")
+
+
 def test_grouped_large_batches():
     # enough rows per group for the largest tiles of every path
     check_grouped((1030, 511, 0, 1290), 512, 768, BF, slack=100, seed=6)

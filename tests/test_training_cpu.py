@@ -105,6 +105,27 @@ def test_grouped_shapes_refused():
     assert L.moe_grouped_workspace_size(None) == 0
 
 
+def test_grouped_matrix_sizes_have_a_limit():
+    # behind it a row's chain of sums drifts past the rounding of its result, and
+    # numbers of column tiles were multiplied past 32 bits (n_in behind 2^25)
+    L = moe.lib()
+    size = lambda c: L.moe_grouped_workspace_size(ctypes.byref(c))  # noqa: E731
+    top = 1 << 20
+    assert size(grouped(rows=1, groups=1, n_in=top, n_out=8)) >= 256
+    assert size(grouped(rows=1, groups=1, n_in=8, n_out=top)) >= 256
+    for big in (top + 8, 1 << 26, (1 << 31) - 8):
+        for n_in, n_out in ((big, 8), (8, big)):
+            bad = grouped(rows=1, groups=1, n_in=n_in, n_out=n_out)
+            assert size(bad) == 0
+            for fn in (L.moe_grouped_matmul, L.moe_grouped_matmul_dx):
+                assert fn(ctypes.byref(bad), *_apart(5), 256, ST) == 2
+            assert L.moe_grouped_matmul_dw(ctypes.byref(bad), *_apart(4), bad.dtype, _fake(), 256,
+                                           ST) == 2
+        for d, F in ((big, 8), (8, big)):
+            c = ctypes.byref(cfg(T=1, d=d, N=1, Z=0, k=1, F=F))
+            assert L.moe_backward_workspace_size(c) == 0
+
+
 def test_grouped_pointers_refused():
     L = moe.lib()
     c = grouped()
