@@ -854,15 +854,18 @@ class AdamW:
     def load_state(self, m, v, step: int):
         """Sets the states (in the layout of ``m`` and ``v``) and the number of
         steps taken."""
+        pairs = []
         for mine, new, name in ((self.m, m, "m"), (self.v, v, "v")):
             mine, new = (mine, new) if self.state_bits == 8 else ((mine,), (new,))
-            if len(mine) != len(new):
+            if not isinstance(new, (tuple, list)) or len(mine) != len(new):
                 raise ValueError(f"{name}: expected (codes, scales)")
             for a, b in zip(mine, new):
                 _need(b, name, a.dtype, a.shape)
-                a.copy_(b)
+                pairs.append((a, b))
         if step < 0:
             raise ValueError(f"step: {step}, expected >= 0")
+        for a, b in pairs:  # nothing is set unless all of it can be
+            a.copy_(b)
         self.state[0] = step
 
 

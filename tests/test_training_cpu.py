@@ -420,6 +420,31 @@ def test_adamw_reads_gradients_where_they_lie(host_adamw):
     assert opt._table is not captured and len(opt._kept) == 1
 
 
+@pytest.mark.parametrize("bits", [32, 8])
+def test_adamw_refused_states_change_nothing(host_adamw, bits):
+    opt = moe.AdamW([torch.ones(300)], [torch.ones(300)], state_bits=bits)
+    e4 = torch.float8_e4m3fn
+    one = lambda v, n=512, k=2: torch.full((n,), v) if bits == 32 else (  # noqa: E731
+        torch.full((n,), v).to(e4), torch.full((k,), v))
+    opt.load_state(one(0.5), one(0.25), 3)
+    held = lambda: [opt.state[0].item()] + [t.float().tolist() for t in (  # noqa: E731
+        (opt.m, opt.v) if bits == 32 else (*opt.m, *opt.v))]
+    before = held()
+    bad = [(one(1.0), one(1.0, 256, 1), 5), (one(1.0, 256, 1), one(1.0), 5),
+           (one(1.0), one(1.0), -1)]
+    if bits == 8:
+        bad += [(one(1.0), one(1.0)[:1], 5), (one(1.0), torch.ones(512), 5),
+                (one(1.0), (one(1.0)[0], torch.ones(3)), 5)]
+    else:
+        bad += [(one(1.0), one(1.0).double(), 5)]
+    for m, v, step in bad:
+        with pytest.raises(ValueError):
+            opt.load_state(m, v, step)
+        assert held() == before
+    opt.load_state(one(1.0), one(2.0), 7)
+    assert held()[0] == 7 and held() != before
+
+
 # ------------------------------------------------------------- the sources --
 def test_arrivals_on_another_cta_release_at_cluster_scope():
     """At a narrower scope nothing that a thread did before its arrival is
