@@ -85,6 +85,10 @@ class GroupedShape:
     dtype: torch.dtype = torch.bfloat16
 
     def c(self) -> MoEGrouped:
+        """A struct of the caller's own."""
+        return MoEGrouped.from_buffer_copy(self._shared())
+
+    def _shared(self) -> MoEGrouped:
         c = self.__dict__.get("_c")  # built once: a frozen shape does not change
         if c is None:
             c = MoEGrouped(self.rows, self.groups, self.n_in, self.n_out,
@@ -110,6 +114,10 @@ class LayerShape:
         return self.n_routed + self.n_zero
 
     def c(self) -> MoEConfig:
+        """A struct of the caller's own."""
+        return MoEConfig.from_buffer_copy(self._shared())
+
+    def _shared(self) -> MoEConfig:
         c = self.__dict__.get("_c")  # built once: a frozen shape does not change
         if c is None:
             c = MoEConfig(self.T, self.d, self.n_routed, self.n_zero, self.top_k, self.ffn,
@@ -250,7 +258,7 @@ def _out(t, name, dtype, shape, device, stream):
 
 
 def workspace_size(shape: LayerShape) -> int:
-    return int(lib().moe_workspace_size(ctypes.byref(shape.c())))
+    return int(lib().moe_workspace_size(ctypes.byref(shape._shared())))
 
 
 def alloc_workspace(shape: LayerShape, device="cuda") -> torch.Tensor:
@@ -262,7 +270,7 @@ def alloc_workspace(shape: LayerShape, device="cuda") -> torch.Tensor:
 
 
 def launch_count(shape: LayerShape) -> int:
-    return int(lib().moe_layer_launch_count(ctypes.byref(shape.c())))
+    return int(lib().moe_layer_launch_count(ctypes.byref(shape._shared())))
 
 
 def route(shape: LayerShape, x, w_router, bias, ws, logits=None, flags=None,
@@ -278,7 +286,7 @@ def route(shape: LayerShape, x, w_router, bias, ws, logits=None, flags=None,
         _need(logits, "logits", torch.float32, (T, E))
     if flags is not None:
         _need(flags, "flags", torch.uint8, (T,))
-    st = lib().moe_route(ctypes.byref(shape.c()), _ptr(x), _ptr(w_router), _ptr(bias),
+    st = lib().moe_route(ctypes.byref(shape._shared()), _ptr(x), _ptr(w_router), _ptr(bias),
                          _ptr(logits), _ptr(idx), _ptr(gate), _ptr(flags), *_ws(ws),
                          _stream(stream))
     _check("moe_route", st)
@@ -301,7 +309,7 @@ def route_noalloc(shape: LayerShape, x, w_router, bias, topk_idx, topk_gate,
         _need(logits, "logits", torch.float32, (T, E))
     if flags is not None:
         _need(flags, "flags", torch.uint8, (T,))
-    st = lib().moe_route_noalloc(ctypes.byref(shape.c()), _ptr(x), _ptr(w_router),
+    st = lib().moe_route_noalloc(ctypes.byref(shape._shared()), _ptr(x), _ptr(w_router),
                                  _ptr(bias), _ptr(logits), _ptr(topk_idx),
                                  _ptr(topk_gate), _ptr(flags), _stream(stream))
     _check("moe_route_noalloc", st)
@@ -319,7 +327,7 @@ def dispatch(shape: LayerShape, x, topk_idx, ws, stream=None):
     row_token = _new((T * k,), i32, dev, stream)
     slot_row = _new((T * k,), i32, dev, stream)
     x_perm = _new((T * k, shape.d), shape.act_dtype, dev, stream)
-    st = lib().moe_dispatch(ctypes.byref(shape.c()), _ptr(x), _ptr(topk_idx),
+    st = lib().moe_dispatch(ctypes.byref(shape._shared()), _ptr(x), _ptr(topk_idx),
                             _ptr(counts), _ptr(offsets), _ptr(row_token),
                             _ptr(slot_row), _ptr(x_perm), *_ws(ws),
                             _stream(stream))
@@ -337,7 +345,7 @@ def expert_ffn(shape: LayerShape, x_perm, offsets, w_gate, w_up, w_down, ws,
                          ("w_down", w_down, (N, d, F))):
         _need(w, name, shape.act_dtype, shp)
     y_perm = _out(y_perm, "y_perm", shape.act_dtype, (T * k, d), x_perm.device, stream)
-    st = lib().moe_expert_ffn(ctypes.byref(shape.c()), _ptr(x_perm), _ptr(offsets),
+    st = lib().moe_expert_ffn(ctypes.byref(shape._shared()), _ptr(x_perm), _ptr(offsets),
                               _ptr(w_gate), _ptr(w_up), _ptr(w_down), _ptr(y_perm),
                               *_ws(ws), _stream(stream))
     _check("moe_expert_ffn", st)
@@ -353,7 +361,7 @@ def combine(shape: LayerShape, x, y_perm, topk_idx, topk_gate, slot_row, out=Non
     _need(topk_gate, "topk_gate", torch.float32, (T, k))
     _need(slot_row, "slot_row", torch.int32, (T * k,))
     out = _out(out, "out", shape.act_dtype, (T, d), x.device, stream)
-    st = lib().moe_combine(ctypes.byref(shape.c()), _ptr(x), _ptr(y_perm),
+    st = lib().moe_combine(ctypes.byref(shape._shared()), _ptr(x), _ptr(y_perm),
                            _ptr(topk_idx), _ptr(topk_gate), _ptr(slot_row), _ptr(out),
                            _stream(stream))
     _check("moe_combine", st)
@@ -363,7 +371,7 @@ def combine(shape: LayerShape, x, y_perm, topk_idx, topk_gate, slot_row, out=Non
 def ep_local_experts(shape: LayerShape, rank: int, world: int) -> int:
     """Routed experts rank `rank` owns when the N routed ids are split evenly
     over `world` ranks (the first N % world ranks take one more)."""
-    n = int(lib().moe_ep_local_experts(ctypes.byref(shape.c()), rank, world))
+    n = int(lib().moe_ep_local_experts(ctypes.byref(shape._shared()), rank, world))
     if n < 0:
         raise ValueError(f"invalid rank {rank} of {world} or shape {shape}")
     return n
@@ -387,7 +395,7 @@ def ep_plan(shape: LayerShape, rank: int, world: int, counts_all, stream=None):
     dev = counts_all.device
     dest_row = _new((N,), torch.int32, dev, stream)
     recv_offsets = _new((ep_local_experts(shape, rank, world) + 1,), torch.int32, dev, stream)
-    st = lib().moe_ep_plan(ctypes.byref(shape.c()), rank, world, _ptr(counts_all),
+    st = lib().moe_ep_plan(ctypes.byref(shape._shared()), rank, world, _ptr(counts_all),
                            _ptr(dest_row), _ptr(recv_offsets), _stream(stream))
     _check("moe_ep_plan", st)
     return dest_row, recv_offsets
@@ -406,7 +414,7 @@ def ep_dispatch(shape: LayerShape, world: int, x, offsets, row_token, dest_row, 
     if len(recv_bufs) != world:
         raise ValueError("one receive buffer per rank")
     ptrs = _pointer_array(recv_bufs, shape.act_dtype, 0, d, x.device)
-    st = lib().moe_ep_dispatch(ctypes.byref(shape.c()), world, _ptr(x), _ptr(offsets),
+    st = lib().moe_ep_dispatch(ctypes.byref(shape._shared()), world, _ptr(x), _ptr(offsets),
                                _ptr(row_token), _ptr(dest_row), _ptr(ptrs), _stream(stream))
     _check("moe_ep_dispatch", st)
     return ptrs  # kept alive by the caller until the stream has run the kernel
@@ -425,7 +433,7 @@ def ep_return(shape: LayerShape, rank: int, world: int, y_recv, recv_offsets, co
     if len(y_homes) != world:
         raise ValueError("one y_perm per rank")
     ptrs = _pointer_array(y_homes, shape.act_dtype, T * k, d, y_recv.device)
-    st = lib().moe_ep_return(ctypes.byref(shape.c()), rank, world, _ptr(y_recv),
+    st = lib().moe_ep_return(ctypes.byref(shape._shared()), rank, world, _ptr(y_recv),
                              _ptr(recv_offsets), _ptr(counts_all), _ptr(offsets_all),
                              _ptr(ptrs), _stream(stream))
     _check("moe_ep_return", st)
@@ -446,7 +454,7 @@ def layer_forward(shape: LayerShape, x, w_router, bias, w_gate, w_up, w_down, ws
     out = _out(out, "out", shape.act_dtype, (T, d), x.device, stream)
     if counts is not None:
         _need(counts, "counts", torch.int32, (E,))
-    st = lib().moe_layer_forward(ctypes.byref(shape.c()), _ptr(x), _ptr(w_router),
+    st = lib().moe_layer_forward(ctypes.byref(shape._shared()), _ptr(x), _ptr(w_router),
                                  _ptr(bias), _ptr(w_gate), _ptr(w_up), _ptr(w_down),
                                  _ptr(out), _ptr(counts), *_ws(ws),
                                  _stream(stream))
@@ -470,7 +478,7 @@ def layer_forward_host(shape: LayerShape, x_host, w_router, bias, w_gate, w_up,
         for name, w, shp in (("w_gate", w_gate, (N, F, d)), ("w_up", w_up, (N, F, d)),
                              ("w_down", w_down, (N, d, F))):
             _need(w, name, shape.act_dtype, shp)
-    st = lib().moe_layer_forward_host(ctypes.byref(shape.c()), _ptr(x_host),
+    st = lib().moe_layer_forward_host(ctypes.byref(shape._shared()), _ptr(x_host),
                                       _ptr(w_router), _ptr(bias), _ptr(w_gate),
                                       _ptr(w_up), _ptr(w_down), _ptr(out_host),
                                       _ptr(counts_host), *_ws(ws),
@@ -503,7 +511,7 @@ def bias_pid_update(shape: LayerShape, counts, bias, state, target: float, kp: f
     _need(bias, "bias", torch.float32, (shape.E,))
     _need(state, "state", torch.float64, (2,))
     prm = MoEPIDParams(target, kp, ki, kd, max_step)
-    st = lib().moe_bias_pid_update(ctypes.byref(shape.c()), _ptr(counts), _ptr(bias),
+    st = lib().moe_bias_pid_update(ctypes.byref(shape._shared()), _ptr(counts), _ptr(bias),
                                    _ptr(state), ctypes.byref(prm), _stream(stream))
     _check("moe_bias_pid_update", st)
     return bias, state
@@ -521,7 +529,7 @@ def _on_current_device(*tensors):
 
 def alloc_grouped_workspace(shape: GroupedShape, device="cuda") -> torch.Tensor:
     """Zeroed workspace of the grouped products (the error word and counters)."""
-    n = int(lib().moe_grouped_workspace_size(ctypes.byref(shape.c())))
+    n = int(lib().moe_grouped_workspace_size(ctypes.byref(shape._shared())))
     if n == 0:
         raise ValueError(f"invalid or unsupported shape {shape}")
     return torch.zeros(n, dtype=torch.uint8, device=device)
@@ -537,7 +545,7 @@ def grouped_matmul(shape: GroupedShape, x, w, offsets, ws, out=None, stream=None
     _need(offsets, "offsets", torch.int32, (G + 1,))
     out = _out(out, "out", shape.dtype, (R, O), x.device, stream)
     _on_current_device(x, w, offsets, ws, out)
-    st = lib().moe_grouped_matmul(ctypes.byref(shape.c()), _ptr(x), _ptr(w), _ptr(offsets),
+    st = lib().moe_grouped_matmul(ctypes.byref(shape._shared()), _ptr(x), _ptr(w), _ptr(offsets),
                                   _ptr(out), *_ws(ws), _stream(stream))
     _check("moe_grouped_matmul", st)
     return out
@@ -552,7 +560,7 @@ def grouped_matmul_dx(shape: GroupedShape, dy, w, offsets, ws, out=None, stream=
     _need(offsets, "offsets", torch.int32, (G + 1,))
     out = _out(out, "out", shape.dtype, (R, I), dy.device, stream)
     _on_current_device(dy, w, offsets, ws, out)
-    st = lib().moe_grouped_matmul_dx(ctypes.byref(shape.c()), _ptr(dy), _ptr(w),
+    st = lib().moe_grouped_matmul_dx(ctypes.byref(shape._shared()), _ptr(dy), _ptr(w),
                                      _ptr(offsets), _ptr(out), *_ws(ws), _stream(stream))
     _check("moe_grouped_matmul_dx", st)
     return out
@@ -569,7 +577,7 @@ def grouped_matmul_dw(shape: GroupedShape, dy, x, offsets, ws, out=None, stream=
     f32 = out is not None and out.dtype == torch.float32
     out = _out(out, "out", torch.float32 if f32 else shape.dtype, (G, O, I), x.device, stream)
     _on_current_device(dy, x, offsets, ws, out)
-    st = lib().moe_grouped_matmul_dw(ctypes.byref(shape.c()), _ptr(dy), _ptr(x),
+    st = lib().moe_grouped_matmul_dw(ctypes.byref(shape._shared()), _ptr(dy), _ptr(x),
                                      _ptr(offsets), _ptr(out), _DTYPE_CODE[out.dtype],
                                      *_ws(ws), _stream(stream))
     _check("moe_grouped_matmul_dw", st)
@@ -579,7 +587,7 @@ def grouped_matmul_dw(shape: GroupedShape, dy, x, offsets, ws, out=None, stream=
 def alloc_backward_workspace(shape: LayerShape, device="cuda") -> torch.Tensor:
     """Workspace of the backward calls (its first 256 bytes zeroed: the error
     word must start at zero)."""
-    n = int(lib().moe_backward_workspace_size(ctypes.byref(shape.c())))
+    n = int(lib().moe_backward_workspace_size(ctypes.byref(shape._shared())))
     if n == 0:
         raise ValueError(f"invalid or unsupported shape {shape}")
     ws = torch.empty(n, dtype=torch.uint8, device=device)
@@ -601,7 +609,7 @@ def combine_backward(shape: LayerShape, dout, x, y_perm, topk_idx, topk_gate, sl
     dy_perm = _out(dy_perm, "dy_perm", shape.act_dtype, (T * k, d), x.device, stream)
     dgate = _out(dgate, "dgate", torch.float32, (T, k), x.device, stream)
     _on_current_device(dout, x, y_perm, topk_idx, topk_gate, slot_row, dy_perm, dgate)
-    st = lib().moe_combine_backward(ctypes.byref(shape.c()), _ptr(dout), _ptr(x),
+    st = lib().moe_combine_backward(ctypes.byref(shape._shared()), _ptr(dout), _ptr(x),
                                     _ptr(y_perm), _ptr(topk_idx), _ptr(topk_gate),
                                     _ptr(slot_row), _ptr(dy_perm), _ptr(dgate),
                                     _stream(stream))
@@ -645,7 +653,7 @@ def expert_ffn_backward(shape: LayerShape, x_perm, offsets, w_gate, w_up, w_down
     dx_perm = _out(dx_perm, "dx_perm", shape.act_dtype, (T * k, d), x_perm.device, stream)
     dws, code = _weight_grads(shape, dw_gate, dw_up, dw_down, x_perm.device, stream)
     _on_current_device(x_perm, offsets, w_gate, w_up, w_down, dy_perm, ws, dx_perm, *dws)
-    st = lib().moe_expert_ffn_backward(ctypes.byref(shape.c()), _ptr(x_perm), _ptr(offsets),
+    st = lib().moe_expert_ffn_backward(ctypes.byref(shape._shared()), _ptr(x_perm), _ptr(offsets),
                                        _ptr(w_gate), _ptr(w_up), _ptr(w_down), _ptr(dy_perm),
                                        _ptr(dx_perm), *[_ptr(t) for t in dws], code,
                                        *_ws(ws), _stream(stream))
@@ -670,7 +678,7 @@ def input_backward(shape: LayerShape, dout, x, w_router, topk_idx, topk_gate, sl
     dw_router = _out(dw_router, "dw_router", torch.float32, (E, d), x.device, stream)
     _on_current_device(dout, x, w_router, topk_idx, topk_gate, slot_row, dgate, dx_perm,
                        ws, dx, dw_router)
-    st = lib().moe_input_backward(ctypes.byref(shape.c()), _ptr(dout), _ptr(x),
+    st = lib().moe_input_backward(ctypes.byref(shape._shared()), _ptr(dout), _ptr(x),
                                   _ptr(w_router), _ptr(topk_idx), _ptr(topk_gate),
                                   _ptr(slot_row), _ptr(dgate), _ptr(dx_perm), _ptr(dx),
                                   _ptr(dw_router), *_ws(ws), _stream(stream))
@@ -702,7 +710,7 @@ def layer_backward(shape: LayerShape, dout, x, w_router, w_gate, w_up, w_down, t
     dws, code = _weight_grads(shape, dw_gate, dw_up, dw_down, x.device, stream)
     _on_current_device(dout, x, w_router, w_gate, w_up, w_down, topk_idx, topk_gate, offsets,
                        slot_row, x_perm, y_perm, ws, dx, dw_router, *dws)
-    st = lib().moe_layer_backward(ctypes.byref(shape.c()), _ptr(dout), _ptr(x),
+    st = lib().moe_layer_backward(ctypes.byref(shape._shared()), _ptr(dout), _ptr(x),
                                   _ptr(w_router), _ptr(w_gate), _ptr(w_up), _ptr(w_down),
                                   _ptr(topk_idx), _ptr(topk_gate), _ptr(offsets),
                                   _ptr(slot_row), _ptr(x_perm), _ptr(y_perm), _ptr(dx),

@@ -339,6 +339,20 @@ def test_tensors_of_another_device_are_refused(monkeypatch):
         moe._on_current_device(here, there)
 
 
+def test_the_struct_of_a_shape_is_the_callers_own():
+    import copy
+    import pickle
+    for sh, field in ((moe.LayerShape(4, 64, 2, 1, 2, 32), "T"),
+                      (moe.GroupedShape(4, 2, 64, 32), "rows")):
+        c = sh.c()
+        setattr(c, field, 1000)
+        assert getattr(sh.c(), field) == 4 and sh == copy.deepcopy(sh)
+        assert getattr(pickle.loads(pickle.dumps(sh)).c(), field) == 4
+    sh = moe.GroupedShape(4, 2, 64, 32)
+    sh.c().n_in = 60  # no longer changes what later calls see
+    moe.alloc_grouped_workspace(sh, device="cpu")
+
+
 # ------------------------------------- the optimizer's buffers, on the host --
 @pytest.fixture
 def host_adamw(monkeypatch):
