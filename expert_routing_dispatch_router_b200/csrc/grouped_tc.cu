@@ -565,7 +565,10 @@ struct RowCfg {
   static constexpr bool PAIR = PAIR_;
   static constexpr int kCtas = PAIR ? 2 : 1;
   static constexpr int BN = BN_;                    // rows of a tile
-  static constexpr int kMerge = PAIR ? 64 : 0;      // rows that may join the last one
+  // rows that may join the last one (16 groups of 2048 x 6144, y and dx: 270 rows
+  // 105 and 112-127 us with, 129 and 141-146 without; 256 and from 330 rows on the
+  // same within 5 %)
+  static constexpr int kMerge = PAIR ? 64 : 0;
   static constexpr int BNH = BN / kCtas;            // rows one CTA loads, and of those
   static constexpr int kMergeH = kMerge / kCtas;    // that join
   static_assert(BNH <= 128 && BN % (16 * kCtas) == 0, "rows of a unit");
@@ -964,6 +967,10 @@ struct DwArgs {
 struct DwCfg {
   static constexpr int kChain = 1024;
   static constexpr int kRun = 8;
+  // Slots of dy and of x, of which shared memory holds twelve. 16 groups of 2048 x
+  // 6144 in bf16, with 4 + 8 / 5 + 7 / 6 + 6: 100 and 500 rows within 3 % of each
+  // other; 200 rows 111 / 111 / 114 us, 270 to 320 rows 142 / 123-128 / 128-131,
+  // 330 to 380 rows 158-176 / 153-172 / 140-150, 400 rows 168 / 163 / 166.
   static constexpr int kASlots = 5, kBSlots = 7;
   static constexpr uint32_t kSlotBytes = 2 * kBlockBytes;  // 128 columns x 64 rows
   static constexpr uint32_t kOutBuf = 4096;  // one warp's 32 rows x 128 bytes
@@ -1413,8 +1420,16 @@ cudaError_t run_rows(const RowMaps& maps, const RowArgs& args, cudaStream_t st) 
 
 template <Mode MODE>
 cudaError_t run_rows_sized(const RowMaps& maps, const RowArgs& args, cudaStream_t st) {
-  // rows per group if they were spread evenly: few rows want small row tiles
-  // (deeper rings while weights stream), many rows want CTA pairs
+  // Rows per group if the capacity were used and spread evenly (how many there
+  // are is known on the device only). 32 groups of 1024 x 4096, y and dx, with
+  // 64-row tiles / 128-row tiles / pairs of 256:
+  //   32 rows    45, 43 /  46,  44 / 49, 51 us: a smaller tile, a deeper ring
+  //   64 rows    47, 44 /  47,  45 / 50, 52
+  //   65 rows    66, 75 /  49,  47 / 51, 53: a second tile loads the weights again
+  //   128 rows   69, 78 /  52,  51 / 53, 56
+  //   129 rows   94, 110 / 74,  80 / 55, 57
+  // At an average of 32 hardly a group has more than 64 rows; at 128 half of
+  // them have more, but few of those more than twice that.
   const int64_t avg = args.rows / args.groups;
   if (avg <= 32) return run_rows<MODE, 64, false>(maps, args, st);
   if (avg <= 128) return run_rows<MODE, 128, false>(maps, args, st);

@@ -463,10 +463,14 @@ T* at(void* ws, size_t off) {
 
 int64_t router_dw_chunks(const Shape& sh) { return sh.T * sh.k / kDwChunk + sh.E; }
 
-// Slots up to which the list is sorted by one block in one launch (with 320
-// experts: 6144 slots 60 against 58 us for the whole call, 12288 slots 110
-// against 86, a quarter of that 36 against 41).
-constexpr int64_t kListOneBlock = 6144;
+// Slots up to which the list is sorted by one block in one launch instead of three
+// kernels. The whole call (d = 2048) with one block / three kernels:
+//   8 experts    2048 slots 39 / 39 us, 4096 slots 49 / 45, 6144 slots 58 / 51
+//   40 experts   2048 slots 26 / 28, 4096 slots 46 / 41, 6144 slots 48 / 44
+//   160 experts  2048 slots 19 / 24, 4096 slots 28 / 28, 6144 slots 35 / 34
+//   320 experts  2048 slots 19 / 26, 4096 slots 25 / 30, 6144 slots 35 / 33
+//   1024 experts 2048 slots 31 / 45, 4096 slots 38 / 50, more do not fit one block
+constexpr int64_t kListOneBlock = 4096;
 
 template <typename AT>
 cudaError_t input_backward(const Shape& sh, const BackwardWs& L, const void* dout,
