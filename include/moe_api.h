@@ -291,7 +291,8 @@ moe_status_t moe_bias_pid_update(const moe_config_t* cfg, const int32_t* counts,
  *  - Sums run in fp32 in an order that does not depend on thread timing. A
  *    result is rounded once, when it is stored; h and the gradients of the
  *    pre-activations are also rounded to the activation type, as h is in the
- *    forward pass.
+ *    forward pass. Weight gradients of bf16 operands that are asked for in float
+ *    are the fp32 sums of such rounded values.
  *
  * Matrix products grouped by expert, in three directions. `groups` matrices
  * w [groups, n_out, n_in] meet row segments [offsets[e], offsets[e+1]):
@@ -426,7 +427,8 @@ moe_status_t moe_layer_backward(const moe_config_t* cfg, const void* dout, const
  *  Returns MOE_ERR_INVALID_ARG for a beta outside [0, 1), a negative or
  *  non-finite lr or weight_decay, an eps outside [2^-126, 1e30], a bad
  *  pointer, or overlapping states. What the table points to cannot be checked
- *  here: weights and masters may overlap nothing else. Host structs are read during the call only. */
+ *  here: weights and masters may overlap nothing else. Host structs are read
+ *  during the call only. */
 typedef struct {
   void* param;
   float* master; /* NULL: param itself is updated */
