@@ -230,6 +230,14 @@ def _ws(ws: torch.Tensor):
     return ctypes.c_void_p(ws.data_ptr()), ws.numel() * ws.element_size()
 
 
+def _on(stream, device=None):
+    """A context in which the call's stream, an object with its handle in
+    `cuda_stream`, is torch's current one."""
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream, device)
+    return torch.cuda.stream(stream)
+
+
 def _new(shape, dtype, device, stream):
     """A new output of a call on `stream`. torch hands out memory stream by
     stream, so it is taken from the call's own: nobody else still uses it when
@@ -241,9 +249,7 @@ def _new(shape, dtype, device, stream):
     current = torch.cuda.current_stream(device)
     if stream.cuda_stream == current.cuda_stream:
         return torch.empty(shape, dtype=dtype, device=device)
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(stream.cuda_stream, device)
-    with torch.cuda.stream(stream):
+    with _on(stream, device):
         t = torch.empty(shape, dtype=dtype, device=device)
     t.record_stream(current)
     return t
@@ -728,7 +734,7 @@ def _capturing(stream=None) -> bool:
     """Whether the call's stream is being captured into a graph."""
     if stream is None:
         return torch.cuda.is_current_stream_capturing()
-    with torch.cuda.stream(stream):
+    with _on(stream):
         return torch.cuda.is_current_stream_capturing()
 
 

@@ -2,6 +2,7 @@
 derives the tolerances): grouped products in three directions, the experts',
 combine's and input's backward passes, the whole layer, and AdamW steps."""
 import math
+import types
 
 import pytest
 import torch
@@ -549,6 +550,44 @@ def test_an_output_dropped_at_once_is_not_handed_out_while_the_call_writes_it():
     mine = [torch.full((8, 512), 7.0, device=DEV) for _ in range(8)]
     torch.cuda.synchronize()
     assert all(bool((t == 7.0).all()) for t in mine) and torch.equal(dx, want)
+
+
+def test_calls_on_a_forked_stream_are_captured():
+    # outputs not given, some dropped at once, on a stream that joins the capture;
+    # and the optimizer on a stream that is only a handle
+    ls = moe.LayerShape(90, 128, 4, 2, 2, 64, BF, 2.0)
+    x, dout, w_r, bias, wg, wu, wd = weights(ls, 37)
+    _, idx, gate, off, slot_row, xp, yp = forward(ls, x, w_r, bias, wg, wu, wd)
+    args = (ls, dout, x, w_r, wg, wu, wd, idx, gate, off, slot_row, xp, yp)
+    ws = moe.alloc_backward_workspace(ls)
+    want = moe.layer_backward(*args, ws)
+    p, grad = torch.ones(500, device=DEV), torch.ones(500, device=DEV)
+    opt = moe.AdamW([p], [grad])
+    side = torch.cuda.Stream()
+    handle = types.SimpleNamespace(cuda_stream=side.cuda_stream)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        moe.layer_backward(*args, ws, stream=side)  # all outputs dropped
+        got = moe.layer_backward(*args, ws, stream=side)
+        moe.adamw_step(opt, lr=0.5, stream=handle)
+        torch.cuda.current_stream().wait_stream(side)
+        copies = [t.clone() for t in got]
+        del got
+    assert opt._captured
+    for _ in range(3):
+        for t in copies:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(copies, want))
+    assert int(opt.state[0]) == 3 and moe.read_device_error(ws) == 0
+    with torch.cuda.stream(side):
+        moe.adamw_step(opt, lr=0.5)
+    y = moe.combine(ls, x, yp, idx, gate, slot_row, stream=handle)
+    torch.cuda.synchronize()
+    assert int(opt.state[0]) == 4 and torch.equal(y, moe.combine(ls, x, yp, idx, gate, slot_row))
 
 
 # ------------------------------------------- positions behind 2^31 elements --
