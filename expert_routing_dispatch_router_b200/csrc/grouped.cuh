@@ -143,8 +143,7 @@ __device__ __forceinline__ int32_t segment_tiles(int32_t rows, int tile, int sla
   return rows <= tile + slack ? 1 : (rows - slack + tile - 1) / tile;
 }
 // The table of offsets that fall, by one thread. Looking whether any falls takes
-// the CUDA-core kernels 0.2 to 1 us (the tiny float layer's backward 52 -> 55 us),
-// the others nothing that shows.
+// the CUDA-core kernels up to 1 us, the others nothing that shows.
 static __device__ __noinline__ void raise_segments(int n, int tile, int slack, int32_t* s_off,
                                                    int32_t* s_tile) {
   if (threadIdx.x == 0) {

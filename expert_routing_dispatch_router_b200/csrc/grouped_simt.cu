@@ -13,13 +13,16 @@
 // share a launch.
 //   kFwd, kDx  tile = rows of one segment x output columns
 //   kDw        tile of one group's matrix; a group without rows contracts
-//              nothing and writes zeros
+//              nothing and writes zeros. The rows are summed in chains of kChain
+//              and the chains' sums added: in one chain over millions of rows of
+//              one sign the terms fall below a step of the sum (1.5e-2 off at
+//              2^24 rows)
 #include "grouped.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kStep = 16, kSimtThreads = 256;
+constexpr int kStep = 16, kSimtThreads = 256, kChain = 1024;
 
 struct SimtArgs {
   GroupedJob job[kMaxJobs];
@@ -164,8 +167,24 @@ __device__ __forceinline__ void run_tile(const GroupedJob& job, int64_t unit, in
   }
   const int64_t wn = (int64_t)n_in * n_out;
   const float* b = static_cast<const float*>(job.b) + (FORM == Form::kDw ? 0 : e * wn);
-  accumulate<TILE, FORM>(static_cast<const float*>(job.a), b, row0, n_rows, i0, j0, n_in, n_out,
-                         sm, acc);
+  const float* a = static_cast<const float*>(job.a);
+  if (FORM == Form::kDw) {
+    float chain[4][4];
+    for (int c0 = 0; c0 < n_rows; c0 += kChain) {
+#pragma unroll
+      for (int p = 0; p < 4; ++p)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) chain[p][q] = 0.f;
+      accumulate<TILE, FORM>(a, b, row0 + c0, n_rows - c0 < kChain ? n_rows - c0 : kChain, i0, j0,
+                             n_in, n_out, sm, chain);
+#pragma unroll
+      for (int p = 0; p < 4; ++p)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) acc[p][q] += chain[p][q];
+    }
+  } else {
+    accumulate<TILE, FORM>(a, b, row0, n_rows, i0, j0, n_in, n_out, sm, acc);
+  }
   if (FORM == Form::kDx && job.a2 != nullptr)
     accumulate<TILE, FORM>(static_cast<const float*>(job.a2),
                            static_cast<const float*>(job.b2) + e * wn, row0, n_rows, i0, j0, n_in,
@@ -237,7 +256,7 @@ __global__ void __launch_bounds__(kSimtThreads)
       run_tile<TILE, Form::kFwd>(j, unit, args.groups, s_off, s_tile, sm);
     else if (j.form == Form::kDx)
       run_tile<TILE, Form::kDx>(j, unit, args.groups, s_off, s_tile, sm);
-    else
+    else if constexpr (TILE == 64)  // weight gradients have these tiles only
       run_tile<TILE, Form::kDw>(j, unit, args.groups, s_off, s_tile, sm);
   }
 }
@@ -266,7 +285,7 @@ cudaError_t launch_grouped_simt(const GroupedShape& g, const GroupedJob* jobs, i
   for (int q = 0; q < kMaxJobs; ++q) a.job[q] = q < n_jobs ? jobs[q] : GroupedJob{};
   // 32 x 32 tiles where 64 x 64 ones would not give every SM two blocks (dx of
   // 8 x 26 rows, 256 columns from 512: 26 -> 12 us with the launch) or would be
-  // half empty on average; large products are faster with 64 x 64 (33 TFLOP/s).
+  // half empty on average; large products are faster with 64 x 64 (34 to 36 TFLOP/s).
   // Weight gradients contract over a segment's rows, often fewer than the four
   // teams' first steps.
   const bool small = jobs[0].form != Form::kDw &&

@@ -125,6 +125,25 @@ def test_grouped_weight_gradient_of_a_long_segment_does_not_drift(dw_dtype):
         ref.check(out[e], want.cpu(), bound.cpu(), dw_dtype, f"dw of {n} rows")
 
 
+def test_grouped_float_weight_gradient_of_a_long_segment_does_not_drift():
+    # the most rows of a call, terms of one sign: in one chain the last terms
+    # are below a step of the sum and are rounded all one way. Chains of 1024
+    # rows and the sum of those chains, every addition rounded (2^-24 each)
+    R, n = 1 << 24, 8
+    g = torch.Generator(device=DEV).manual_seed(53)
+    x, dy = (torch.rand(R, n, generator=g, device=DEV) * 0.5 + 0.5 for _ in range(2))
+    off = dev(torch.tensor([0, 1000, R], dtype=torch.int32))
+    sh = moe.GroupedShape(R, 2, n, n, F32)
+    ws = moe.alloc_grouped_workspace(sh)
+    dw = moe.grouped_matmul_dw(sh, dy, x, off, ws)
+    assert moe.read_device_error(ws) == 0
+    for e, lo, hi in ref.segments(off):
+        want = sum(dy[i:min(i + 2 ** 20, hi)].double().T @ x[i:min(i + 2 ** 20, hi)].double()
+                   for i in range(lo, hi, 2 ** 20))
+        bound = (1024 + (hi - lo) // 1024 + 1) * ref.U / 2 * want
+        ref.check(dw[e], want.cpu(), bound.cpu(), F32, f"dw of {hi - lo} rows")
+
+
 @pytest.mark.parametrize("n_in,n_out", [(1 << 20, 8), (8, 1 << 20)])
 def test_grouped_widest_matrices(n_in, n_out):
     # terms of one sign; a product of 2^20 terms is 2^16 additions of 16, each
