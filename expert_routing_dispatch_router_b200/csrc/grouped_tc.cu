@@ -261,13 +261,21 @@ struct Cg<true> {
 
 // Bounded wait on an mbarrier phase. False when the CTA was told to stop, or
 // when the limit ran out (then it tells the CTA to stop and records the error).
+// In a CTA pair (PAIR) with acquire at cluster scope: the other CTA takes part in
+// most phases, by arrivals, commits or copies, and what it did before is ordered
+// before what follows here. (CTA scope for those that it does not: no faster.)
+template <bool PAIR>
+__device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
+  return PAIR ? ptx::mbar_try_wait_cluster(bar, parity) : ptx::mbar_try_wait(bar, parity);
+}
+template <bool PAIR>
 __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity,
                                              volatile int* abort_flag, int32_t* err) {
-  if (ptx::mbar_try_wait(bar, parity)) return true;
+  if (try_wait<PAIR>(bar, parity)) return true;
   const uint64_t t0 = ptx::global_timer_ns();
   while (true) {
     for (int i = 0; i < 64; ++i)
-      if (ptx::mbar_try_wait(bar, parity)) return true;
+      if (try_wait<PAIR>(bar, parity)) return true;
     if (*abort_flag) return false;
     if (ptx::global_timer_ns() - t0 > kWaitLimitNs) {
       *abort_flag = 1;
@@ -278,33 +286,10 @@ __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity,
 }
 
 // The same by a whole warp; every lane gets the same answer.
+template <bool PAIR>
 __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile int* abort_flag,
                                           int32_t* err) {
-  return __all_sync(0xffffffffu, wait_bounded(bar, parity, abort_flag, err));
-}
-
-// The same with cluster-scope acquire, for a phase that the other CTA of the
-// pair takes part in: what it did before its arrival is ordered before what
-// follows here.
-__device__ __forceinline__ bool wait_bounded_cluster(uint32_t bar, uint32_t parity,
-                                                     volatile int* abort_flag, int32_t* err) {
-  if (ptx::mbar_try_wait_cluster(bar, parity)) return true;
-  const uint64_t t0 = ptx::global_timer_ns();
-  while (true) {
-    for (int i = 0; i < 64; ++i)
-      if (ptx::mbar_try_wait_cluster(bar, parity)) return true;
-    if (*abort_flag) return false;
-    if (ptx::global_timer_ns() - t0 > kWaitLimitNs) {
-      *abort_flag = 1;
-      atomicCAS(err, 0, kErrWaitTimeout);
-      return false;
-    }
-  }
-}
-
-__device__ __forceinline__ bool wait_warp_cluster(uint32_t bar, uint32_t parity,
-                                                  volatile int* abort_flag, int32_t* err) {
-  return __all_sync(0xffffffffu, wait_bounded_cluster(bar, parity, abort_flag, err));
+  return __all_sync(0xffffffffu, wait_bounded<PAIR>(bar, parity, abort_flag, err));
 }
 
 // Whether an mbarrier phase is complete, without waiting.
@@ -364,9 +349,7 @@ struct Control {
   __device__ bool publish(int seq, int u, int32_t* err) const {
     const int r = seq % kRing;
     const uint32_t par = (uint32_t)(seq / kRing) & 1u;
-    if (PAIR ? !wait_bounded_cluster(ring_empty(r), par ^ 1u, abort_flag, err)
-             : !wait_bounded(ring_empty(r), par ^ 1u, abort_flag, err))
-      return false;
+    if (!wait_bounded<PAIR>(ring_empty(r), par ^ 1u, abort_flag, err)) return false;
     ring[r] = u;
     if (PAIR) {
       ptx::st_shared_cluster_u32(
@@ -379,9 +362,7 @@ struct Control {
   __device__ bool take(int seq, int* u, int32_t* err) const {
     const int r = seq % kRing;
     const uint32_t par = (uint32_t)(seq / kRing) & 1u;
-    if (PAIR ? !wait_bounded_cluster(ring_full(r), par, abort_flag, err)
-             : !wait_bounded(ring_full(r), par, abort_flag, err))
-      return false;
+    if (!wait_bounded<PAIR>(ring_full(r), par, abort_flag, err)) return false;
     *u = ring[r];
     ptx::mbar_arrive(ring_empty(r));
     return true;
@@ -429,10 +410,9 @@ struct Control {
       }
     }
   }
-  // The MMA warp's wait for accumulator b.
-  __device__ bool wait_released(int b, uint32_t parity, int32_t* err) const {
-    return PAIR ? wait_warp_cluster(tempty(b), parity, abort_flag, err)
-                : wait_warp(tempty(b), parity, abort_flag, err);
+  // A warp's wait for a phase.
+  __device__ bool wait(uint32_t bar, uint32_t parity, int32_t* err) const {
+    return wait_warp<PAIR>(bar, parity, abort_flag, err);
   }
   // Next unit for the producer warp: the leader publishes the one it claimed
   // before, then claims another (after the arrivals, which would wait for the
@@ -702,7 +682,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // weights that only this unit reads (one row tile) are streamed
       const uint64_t pol_w = un.ntiles == 1 ? pol_first : pol_normal;
       for (int kb = 0; kb < n_kb; ++kb) {
-        if (!(ok = wait_warp(ctl.empty(stage), phase ^ 1u, ctl.abort_flag, args.err))) break;
+        if (!(ok = ctl.wait(ctl.empty(stage), phase ^ 1u, args.err))) break;
         const int src = kb >= args.k_blocks ? 1 : 0;
         const int k0 = (kb - src * args.k_blocks) * BK;
         if (elected) {
@@ -759,9 +739,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok || u < 0) break;
         const RowUnit un = row_unit<BN>(u, s_tile, s_off, args.groups, m_tiles);
         const int n0 = mma_rows(un.n, 0), n1 = PAIR ? mma_rows(un.n, 1) : 0;
-        if (!(ok = ctl.wait_released(slot & 1, ((slot >> 1) & 1u) ^ 1u, args.err))) break;
-        if (n1 > 0 && !(ok = ctl.wait_released((slot + 1) & 1, (((slot + 1) >> 1) & 1u) ^ 1u,
-                                               args.err)))
+        if (!(ok = ctl.wait(ctl.tempty(slot & 1), ((slot >> 1) & 1u) ^ 1u, args.err))) break;
+        if (n1 > 0 && !(ok = ctl.wait(ctl.tempty((slot + 1) & 1),
+                                      (((slot + 1) >> 1) & 1u) ^ 1u, args.err)))
           break;
         ptx::tc_fence_after();
         const uint32_t i0 = ptx::idesc_bf16_f32(BM * C::kCtas, n0) | kFlags;
@@ -769,7 +749,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t d0 = tmem_base + (slot & 1) * kAccStride;
         const uint32_t d1 = tmem_base + ((slot + 1) & 1) * kAccStride;
         for (int kb = 0; kb < n_kb; ++kb) {
-          if (!(ok = wait_warp(ctl.full(stage), phase, ctl.abort_flag, args.err))) break;
+          if (!(ok = ctl.wait(ctl.full(stage), phase, args.err))) break;
           ptx::tc_fence_after();
           if (elected) {
             const uint32_t a0 = sbase + stage * C::kStageBytes;
@@ -843,8 +823,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         };
         if (MODE == Mode::kSwiglu) fetch(0);  // while the unit's products still run
-        ok = __all_sync(0xffffffffu, wait_bounded(ctl.tfull(slot & 1), (slot >> 1) & 1u,
-                                                  ctl.abort_flag, args.err));
+        ok = ctl.wait(ctl.tfull(slot & 1), (slot >> 1) & 1u, args.err);
         if (!ok) break;
         ptx::tc_fence_after();
         if (MODE == Mode::kSwiglu) {
@@ -1125,7 +1104,7 @@ __global__ void __launch_bounds__(kDwThreads, 1)
         for (int k0 = 0; k0 < un.n_rows; k0 += BK) {
           const int n = un.n_rows - k0 < BK ? un.n_rows - k0 : BK;
           const int at = base + slot;
-          if (!(ok = wait_warp(ctl.empty(at), phase ^ 1u, ctl.abort_flag, args.err))) break;
+          if (!(ok = ctl.wait(ctl.empty(at), phase ^ 1u, args.err))) break;
           if (elected) {
             if (rank == 0)
               ptx::mbar_arrive_expect_tx(ctl.full(at),
@@ -1169,13 +1148,13 @@ __global__ void __launch_bounds__(kDwThreads, 1)
             pa = pa0;
           }
           for (int c0 = 0; c0 < un.n_rows && ok; c0 += C::kChain) {
-            if (!(ok = ctl.wait_released(acc, acc_phase ^ 1u, args.err))) break;
+            if (!(ok = ctl.wait(ctl.tempty(acc), acc_phase ^ 1u, args.err))) break;
             ptx::tc_fence_after();
             const uint32_t d0 = tmem_base + (uint32_t)acc * kAccStride;
             const int rows = un.n_rows - c0 < C::kChain ? un.n_rows - c0 : C::kChain;
             for (int k0 = 0; k0 < rows; k0 += BK) {
-              if (load_a && !(ok = wait_warp(ctl.full(sa), pa, ctl.abort_flag, args.err))) break;
-              if (!(ok = wait_warp(ctl.full(SA + sb), pb, ctl.abort_flag, args.err))) break;
+              if (load_a && !(ok = ctl.wait(ctl.full(sa), pa, args.err))) break;
+              if (!(ok = ctl.wait(ctl.full(SA + sb), pb, args.err))) break;
               ptx::tc_fence_after();
               const int left = rows - k0;
               if (elected) {
@@ -1243,8 +1222,7 @@ __global__ void __launch_bounds__(kDwThreads, 1)
 #pragma unroll
           for (int c = 0; c < 32; ++c) sum[q][c] = 0.f;
         for (int c0 = 0; c0 < un.n_rows; c0 += C::kChain) {
-          ok = __all_sync(0xffffffffu,
-                          wait_bounded(ctl.tfull(acc), acc_phase, ctl.abort_flag, args.err));
+          ok = ctl.wait(ctl.tfull(acc), acc_phase, args.err);
           if (!ok) break;
           ptx::tc_fence_after();
           const uint32_t tb = tmem_base + (static_cast<uint32_t>(ew * 32) << 16) +
